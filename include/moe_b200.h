@@ -404,6 +404,132 @@ moe_status moe_backward(const moe_config* cfg, const moe_weights* w, const moe_b
                         size_t workspace_bytes, void* stream);
 
 /*
+ * Routing by softmax or sigmoid scores (the DeepSeekV3MoE bullet's router in the forms
+ * moe_route does not have).  From the logits l of a token:
+ *   score  MOE_SCORE_SIGMOID: s = 1 / (1 + exp(-l)); MOE_SCORE_SOFTMAX: the softmax of the
+ *          row.  A logit of -inf or NaN is a masked expert: it has no score (and no part in
+ *          the softmax's sum) and is never selected.
+ *   key    the logit without a bias, score + bias with one; a bias of -inf or NaN takes the
+ *          expert out of the selection for every token.
+ *   groups the topk_group of n_group groups with the largest sum of their group_top (1 or 2)
+ *          largest keys (without a bias and with group_top 2: scores), over the experts that
+ *          can be selected; a group without any is not kept.
+ *   gates  routed_scaling_factor * score, divided by the sum over the selected when
+ *          renormalize is 1 (a ratio that holds also where the scores are too small for any
+ *          type).
+ * The top_k largest keys are listed in descending order, equal ones (and equal groups) by
+ * the lower index.  Where fewer experts can be selected, the places left hold index -1 and
+ * gate 0 (moe_permute leaves such places out and reports them like any index outside
+ * [0, E)).  The selection is the one of exact arithmetic as far as 64 bits resolve it: a row
+ * whose keys come too near to each other for 32 bits is scored again in 64.
+ */
+typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
+
+typedef struct moe_router {
+  int32_t score;        /* moe_score */
+  int32_t renormalize;  /* 0 or 1 */
+  int32_t group_top;    /* 1 or 2; not used when n_group is 1 */
+} moe_router;
+
+/*
+ * Arguments as moe_route's, with these differences: bias may be NULL; with logits_in the
+ * workspace is not used and may be NULL.
+ */
+moe_status moe_route_scored(const moe_config* cfg, const moe_router* router, const void* x,
+                            const void* w_router, const float* bias, const float* logits_in,
+                            float* logits_out, int32_t* topk_idx, float* topk_w, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of moe_route_scored's gates with respect to the logits: dgate [T, top_k] fp32 ->
+ * dlogits [T, E] fp32 (every element written).  The selection and the bias get no gradient
+ * (piecewise constant).  With g_j = routed_scaling_factor * dgate_j on the selected places:
+ *   ds_j = (g_j - sum_i g_i s_i / S) / S with S = sum of the selected s (renormalize 1), or
+ *   ds_j = g_j;
+ *   dlogit_e = ds_e s_e (1 - s_e) (sigmoid), s_e (ds_e - sum_i ds_i s_i) (softmax).
+ * Places of topk_idx outside [0, E), or that name a masked expert, have no gradient; places
+ * that name one expert twice add up.
+ * dscore (NULL: none): adds the gradient of moe_balance_loss, whose outputs it is:
+ * [n_seq, E] fp32, with seq_offsets and n_seq as there and *dloss (device fp32, NULL: 1) the
+ * gradient of what follows with respect to the loss.  With c_e = dloss * dscore[q, e] for
+ * the token's sequence q and s' = s / sum_e s:
+ *   dlogit_e += s_e (1 - s_e) / sum_i s_i * (c_e - sum_i c_i s'_i)  (sigmoid),
+ *   dlogit_e += s_e (c_e - sum_i c_i s_i)                           (softmax).
+ */
+moe_status moe_route_backward(const moe_config* cfg, const moe_router* router, const float* logits,
+                              const int32_t* topk_idx, const float* dgate, const float* dscore,
+                              const int32_t* seq_offsets, int32_t n_seq, const float* dloss,
+                              float* dlogits, void* stream);
+
+/*
+ * Balance loss per sequence (TransformerEngine PR "DeepSeekV3Layer": the sequence-wise
+ * auxiliary loss it leaves to a follow-up).  Sequence q holds the rows seq_offsets[q] ..
+ * seq_offsets[q + 1] - 1 ([n_seq + 1] int32 on the device, ascending, inside [0, T];
+ * sequences may be empty, and rows outside all of them do not count); seq_offsets NULL: one
+ * sequence of all T rows (n_seq 1).  Over the n_q rows of q that have a score at all:
+ *   load[q, e] = places of topk_idx that name e;   f = E / (top_k n_q) * load;
+ *   P[q, e] = mean of s'_te = s_te / sum_e s_te;
+ *   loss = coef / n_seq * sum_q sum_e f P                       ([1] fp32);
+ *   dscore[q, e] = coef / n_seq * f / n_q, the gradient of the loss with respect to each
+ *   s'_te of q's rows, which moe_route_backward reads             ([n_seq, E] fp32).
+ * load is [n_seq, E] int32 (its sum over q is what a bias update reads).  Every sum has an
+ * order of its own that the shape fixes: equal inputs give equal bits.  workspace:
+ * moe_balance_workspace_size bytes, which need not be zero.
+ */
+moe_status moe_balance_workspace_size(const moe_config* cfg, int32_t n_seq, size_t* bytes);
+moe_status moe_balance_loss(const moe_config* cfg, const moe_router* router, const float* logits,
+                            const int32_t* topk_idx, const int32_t* seq_offsets, int32_t n_seq,
+                            float coef, float* loss, int32_t* load, float* dscore, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * Orthogonalised updates (the Muon optimiser's, for the weight gradients moe_backward
+ * writes): each of `groups` stacked row-major matrices [rows, cols] is divided by its
+ * Frobenius norm + eps and taken through `steps` steps of
+ *   X <- a X + (b A + c A^2) X, A = X X^T   (rows > cols: the same from the other side),
+ * which move its singular values towards 1.  The usual coefficients are a = 3.4445,
+ * b = -4.7750, c = 2.0315 with 5 steps and eps 1e-7.
+ * fp16 operands with power-of-two scales and fp32 accumulation; the linear term a X is
+ * carried in 22 bits.  Results differ from exact arithmetic by about 1e-3 of their norm
+ * before the bf16 rounding (more where that norm is below eps / 1000: all values are near 0
+ * then).  A zero
+ * matrix stays zero; an infinity or NaN stays in its matrix.
+ *
+ * Supported: groups <= 65535, rows * cols (rounded up to 8) <= 2^30, 1 <= steps <= 64,
+ * 0 < eps < 1, and coefficients that keep |singular values| below 1.9 and |b x + c x^2| below
+ * 7.9 from [0, 1] on, step by step (MOE_ERR_UNSUPPORTED otherwise).
+ */
+typedef struct moe_muon_config {
+  int32_t groups, rows, cols;
+  int32_t steps;
+  float a, b, c;
+  float eps;
+} moe_muon_config;
+
+typedef enum { MOE_GRAD_FP32 = 0, MOE_GRAD_BF16 = 1 } moe_grad_dtype;
+
+/*
+ * workspace: moe_muon_workspace_size bytes, its first 4 bytes (the status word) zero before
+ * the first call; calls that may overlap need workspaces of their own.
+ */
+moe_status moe_muon_workspace_size(const moe_muon_config* cfg, size_t* bytes);
+
+/* out [groups, rows, cols] bf16 = the orthogonalised g (fp32 or bf16, g_dtype). */
+moe_status moe_orthogonalize(const moe_muon_config* cfg, const void* g, int32_t g_dtype, void* out,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One optimiser step: m' = beta momentum_in + grad; u = grad + beta m' (nesterov 1) or m';
+ * w_out = (1 - decay) w_in - step * orthogonalised(u), rounded once.  momentum fp32, w bf16,
+ * grad fp32 or bf16 (grad_dtype), all [groups, rows, cols]; momentum_out may be momentum_in
+ * and w_out may be w_in (in place), other overlaps are not allowed.  0 <= beta < 1.
+ */
+moe_status moe_muon_step(const moe_muon_config* cfg, const void* grad, int32_t grad_dtype,
+                         const float* momentum_in, float* momentum_out, float beta,
+                         int32_t nesterov, const void* w_in, void* w_out, float step, float decay,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Reads (and clears) the device status word at the start of `workspace`.
  * Synchronizes `stream`.  *device_status receives a moe_status value.
  */

@@ -39,4 +39,13 @@ from .binding import (  # noqa: F401
     prepare_backward_weights,
     moe_backward_workspace_size,
     moe_backward,
+    MoERouter,
+    moe_route_scored,
+    moe_route_backward,
+    moe_balance_workspace_size,
+    moe_balance_loss,
+    MoEMuonConfig,
+    moe_muon_workspace_size,
+    moe_orthogonalize,
+    moe_muon_step,
 )

@@ -70,6 +70,25 @@ class MoEFwdSaved(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _SAVED_FIELDS]
 
 
+SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+class MoERouter(ctypes.Structure):
+    """Options of the scored router: score 0 sigmoid or 1 softmax, renormalize 0 or 1,
+    group_top 1 or 2 (keys of a group that its score sums)."""
+
+    _fields_ = [("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("group_top", ctypes.c_int32)]
+
+
+class MoEMuonConfig(ctypes.Structure):
+    """A stack of matrices and the steps that orthogonalise them."""
+
+    _fields_ = [("groups", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float),
+                ("c", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 _GRAD_FIELDS = ("dw1", "dw3", "dw2", "dws1", "dws3", "dws2", "dw_router")
 
 
@@ -88,6 +107,8 @@ def config_from_shape(s, T=None) -> MoEConfig:
 _lib = None
 _VP = ctypes.c_void_p
 _CFG = ctypes.POINTER(MoEConfig)
+_RTR = ctypes.POINTER(MoERouter)
+_MUON = ctypes.POINTER(MoEMuonConfig)
 
 
 def lib() -> ctypes.CDLL:
@@ -133,6 +154,20 @@ def lib() -> ctypes.CDLL:
                               ctypes.POINTER(MoEFwdSaved), _VP, _VP, _VP, _VP,
                               ctypes.POINTER(MoEWeightGrads), _VP, ctypes.c_size_t, _VP],
                              ctypes.c_int),
+            "moe_route_scored": ([_CFG, _RTR, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                  ctypes.c_size_t, _VP], ctypes.c_int),
+            "moe_route_backward": ([_CFG, _RTR, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP,
+                                    _VP, _VP], ctypes.c_int),
+            "moe_balance_workspace_size": ([_CFG, ctypes.c_int32,
+                                            ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
+            "moe_balance_loss": ([_CFG, _RTR, _VP, _VP, _VP, ctypes.c_int32, ctypes.c_float, _VP,
+                                  _VP, _VP, _VP, ctypes.c_size_t, _VP], ctypes.c_int),
+            "moe_muon_workspace_size": ([_MUON, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
+            "moe_orthogonalize": ([_MUON, _VP, ctypes.c_int32, _VP, _VP, ctypes.c_size_t, _VP],
+                                  ctypes.c_int),
+            "moe_muon_step": ([_MUON, _VP, ctypes.c_int32, _VP, _VP, ctypes.c_float,
+                               ctypes.c_int32, _VP, _VP, ctypes.c_float, ctypes.c_float, _VP,
+                               ctypes.c_size_t, _VP], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -403,6 +438,114 @@ def moe_backward(cfg, weights, bwd_weights, saved: dict, dy, dx, workspace, dlog
         _p(_cuda(dlogits, torch.float32, "dlogits")), _p(_cuda(dgate, torch.float32, "dgate")),
         ctypes.byref(gr) if gr is not None else None, _p(workspace), workspace.numel(),
         _stream(stream)))
+
+
+def _sized(t, dtype, shape, name):
+    """_cuda with the shape checked too (the C call sees only the pointer)."""
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    return _p(_cuda(t, dtype, name))
+
+
+def moe_route_scored(cfg, router, topk_idx, topk_w, x=None, w_router=None, bias=None,
+                     workspace=None, logits_in=None, logits_out=None, stream=None):
+    """Routing by softmax or sigmoid scores: from x and w_router (with a workspace and
+    logits_out), or from the logits alone (logits_in)."""
+    bf, f32, T, E = torch.bfloat16, torch.float32, cfg.T, cfg.E
+    k = cfg.top_k
+    _check("moe_route_scored", lib().moe_route_scored(
+        ctypes.byref(cfg), ctypes.byref(router), _sized(x, bf, (T, cfg.H), "x"),
+        _sized(w_router, bf, (E, cfg.H), "w_router"), _sized(bias, f32, (E,), "bias"),
+        _sized(logits_in, f32, (T, E), "logits_in"),
+        _sized(logits_out, f32, (T, E), "logits_out"),
+        _sized(topk_idx, torch.int32, (T, k), "topk_idx"), _sized(topk_w, f32, (T, k), "topk_w"),
+        _p(workspace), workspace.numel() if workspace is not None else 0, _stream(stream)))
+
+
+def _sequences(seq_offsets, name="seq_offsets"):
+    if seq_offsets is None:
+        return None, 1
+    if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+        raise ValueError(f"{name}: expected at least two offsets in one dimension")
+    return _p(_cuda(seq_offsets, torch.int32, name)), seq_offsets.numel() - 1
+
+
+def moe_route_backward(cfg, router, logits, topk_idx, dgate, dlogits, dscore=None,
+                       seq_offsets=None, dloss=None, stream=None):
+    """dgate -> dlogits of the scored router; with ``dscore`` (of moe_balance_loss, for the
+    same ``seq_offsets``) plus the balance loss's gradient, times the device scalar ``dloss``."""
+    f32, T, E, k = torch.float32, cfg.T, cfg.E, cfg.top_k
+    off, n_seq = _sequences(seq_offsets)
+    _check("moe_route_backward", lib().moe_route_backward(
+        ctypes.byref(cfg), ctypes.byref(router), _sized(logits, f32, (T, E), "logits"),
+        _sized(topk_idx, torch.int32, (T, k), "topk_idx"), _sized(dgate, f32, (T, k), "dgate"),
+        _sized(dscore, f32, (n_seq, E), "dscore"), off, n_seq, _p(_cuda(dloss, f32, "dloss")),
+        _sized(dlogits, f32, (T, E), "dlogits"), _stream(stream)))
+
+
+def moe_balance_workspace_size(cfg, n_seq=1) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_balance_workspace_size",
+           lib().moe_balance_workspace_size(ctypes.byref(cfg), n_seq, ctypes.byref(n)))
+    return n.value
+
+
+def moe_balance_loss(cfg, router, logits, topk_idx, coef, loss, load, dscore, workspace,
+                     seq_offsets=None, stream=None):
+    """Balance loss [1], load [n_seq, E] and dscore [n_seq, E] of the routed rows."""
+    f32, i32, T, E = torch.float32, torch.int32, cfg.T, cfg.E
+    off, n_seq = _sequences(seq_offsets)
+    _check("moe_balance_loss", lib().moe_balance_loss(
+        ctypes.byref(cfg), ctypes.byref(router), _sized(logits, f32, (T, E), "logits"),
+        _sized(topk_idx, i32, (T, cfg.top_k), "topk_idx"), off, n_seq, coef,
+        _sized(loss, f32, (1,), "loss"), _sized(load, i32, (n_seq, E), "load"),
+        _sized(dscore, f32, (n_seq, E), "dscore"), _p(workspace), workspace.numel(),
+        _stream(stream)))
+
+
+GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def moe_muon_workspace_size(mcfg) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_muon_workspace_size",
+           lib().moe_muon_workspace_size(ctypes.byref(mcfg), ctypes.byref(n)))
+    return n.value
+
+
+def _grad(mcfg, t, name):
+    if t.dtype not in GRAD_DTYPES:
+        raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return _stacked(mcfg, t, t.dtype, name), GRAD_DTYPES[t.dtype]
+
+
+def _stacked(mcfg, t, dtype, name):
+    """A contiguous stack of the config's matrices (a single matrix may be 2-D)."""
+    shape = (mcfg.groups, mcfg.rows, mcfg.cols)
+    if tuple(t.shape) != shape and not (mcfg.groups == 1 and tuple(t.shape) == shape[1:]):
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    return _p(_cuda(t, dtype, name))
+
+
+def moe_orthogonalize(mcfg, g, out, workspace, stream=None):
+    """out (bf16) = each matrix of g (fp32 or bf16) with its singular values moved to about 1."""
+    gp, gd = _grad(mcfg, g, "g")
+    _check("moe_orthogonalize", lib().moe_orthogonalize(
+        ctypes.byref(mcfg), gp, gd, _stacked(mcfg, out, torch.bfloat16, "out"), _p(workspace),
+        workspace.numel(), _stream(stream)))
+
+
+def moe_muon_step(mcfg, grad, momentum, momentum_out, w, w_out, workspace, beta=0.95,
+                  nesterov=True, step=0.02, decay=0.0, stream=None):
+    """Momentum, orthogonalised update and weights of one optimiser step; ``momentum_out`` may
+    be ``momentum`` and ``w_out`` may be ``w``."""
+    gp, gd = _grad(mcfg, grad, "grad")
+    f32, bf = torch.float32, torch.bfloat16
+    _check("moe_muon_step", lib().moe_muon_step(
+        ctypes.byref(mcfg), gp, gd, _stacked(mcfg, momentum, f32, "momentum"),
+        _stacked(mcfg, momentum_out, f32, "momentum_out"), beta, 1 if nesterov else 0,
+        _stacked(mcfg, w, bf, "w"), _stacked(mcfg, w_out, bf, "w_out"), step, decay,
+        _p(workspace), workspace.numel(), _stream(stream)))
 
 
 class MoELayer:

@@ -8,13 +8,16 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "backward.cuh"
 #include "grouped_gemm.cuh"
+#include "muon.cuh"
 #include "prepare.cuh"
 #include "quantize.cuh"
 #include "route_permute_combine.cuh"
+#include "route_scored.cuh"
 #include "wgrad.cuh"
 
 using namespace moe;
@@ -392,41 +395,48 @@ int32_t* status_ptr(void* ws) { return static_cast<int32_t*>(ws); }
 // ---------------------------------------------------------------------------
 // Step implementations (arguments already validated).
 // ---------------------------------------------------------------------------
+// Router GEMM x . W_r^T into the workspace: *n_splits partial sums of [T, E].
+moe_status router_gemm(const moe_config& c, const void* x, const void* w_router, void* ws,
+                       cudaStream_t s, const float** partials_out, int* n_splits) {
+  const StepLayout L = step_layout(c);
+  float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.router_partials);
+  GemmParams p;
+  memset(&p, 0, sizeof(p));
+  MOE_TRY(make_map(&p.a0[1], w_router, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.H, c.E,
+                   static_cast<uint64_t>(c.H) * 2, kBM));
+  MOE_TRY(make_map(&p.b[1], x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.H, c.T,
+                   static_cast<uint64_t>(c.H) * 2, kBoxRows));
+  p.a0[0] = p.a1[0] = p.a1[1] = p.a0[1];
+  p.b[0] = p.b[1];
+  GemmGroup g;
+  g.a_rows_per_expert = 0;
+  g.a_valid_rows = c.E;
+  g.n_slabs = (c.E + kBM - 1) / kBM;
+  g.k_tiles = c.H / kBK;
+  g.k_splits = L.router_splits;
+  g.out = partials;
+  g.out_ld = c.E;
+  g.split_stride = static_cast<int64_t>(c.T) * c.E;
+  p.g[0] = p.g[1] = g;
+  p.E = 0;
+  p.dense_rows = c.T;
+  p.status = status_ptr(ws);
+  const int tn = router_tile_of(c);
+  const int units = ((c.T + tn - 1) / tn) * g.n_slabs * g.k_splits;
+  if (tn == 256) MOE_TRY((launch_gemm<kRouter, 256, kBF16>(p, units, s)));
+  else MOE_TRY((launch_gemm<kRouter, 64, kBF16>(p, units, s)));
+  *partials_out = partials;
+  *n_splits = L.router_splits;
+  return MOE_OK;
+}
+
 moe_status do_route(const moe_config& c, const void* x, const void* w_router, const float* bias,
                     const float* logits_in, float* logits_out, int32_t* topk_idx, float* topk_w,
                     void* ws, cudaStream_t s) {
   SelArgs a;
   memset(&a, 0, sizeof(a));
   if (!logits_in) {
-    const StepLayout L = step_layout(c);
-    float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.router_partials);
-    GemmParams p;
-    memset(&p, 0, sizeof(p));
-    MOE_TRY(make_map(&p.a0[1], w_router, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.H, c.E,
-                     static_cast<uint64_t>(c.H) * 2, kBM));
-    MOE_TRY(make_map(&p.b[1], x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.H, c.T,
-                     static_cast<uint64_t>(c.H) * 2, kBoxRows));
-    p.a0[0] = p.a1[0] = p.a1[1] = p.a0[1];
-    p.b[0] = p.b[1];
-    GemmGroup g;
-    g.a_rows_per_expert = 0;
-    g.a_valid_rows = c.E;
-    g.n_slabs = (c.E + kBM - 1) / kBM;
-    g.k_tiles = c.H / kBK;
-    g.k_splits = L.router_splits;
-    g.out = partials;
-    g.out_ld = c.E;
-    g.split_stride = static_cast<int64_t>(c.T) * c.E;
-    p.g[0] = p.g[1] = g;
-    p.E = 0;
-    p.dense_rows = c.T;
-    p.status = status_ptr(ws);
-    const int tn = router_tile_of(c);
-    const int units = ((c.T + tn - 1) / tn) * g.n_slabs * g.k_splits;
-    if (tn == 256) MOE_TRY((launch_gemm<kRouter, 256, kBF16>(p, units, s)));
-    else MOE_TRY((launch_gemm<kRouter, 64, kBF16>(p, units, s)));
-    a.partials = partials;
-    a.n_splits = L.router_splits;
+    MOE_TRY(router_gemm(c, x, w_router, ws, s, &a.partials, &a.n_splits));
     a.logits_out = logits_out;
   } else {
     a.logits = logits_in;
@@ -1372,3 +1382,7 @@ extern "C" moe_status moe_permute_noalloc(const moe_config* cfg, const int32_t* 
 
 // The backward of the bf16 layer: its host steps and its C ABI.
 #include "backward_api.cuh"
+
+// The scored router with its gradient and the balance loss, and the orthogonalised updates.
+#include "route_scored_api.cuh"
+#include "muon_api.cuh"
