@@ -483,6 +483,27 @@ moe_status moe_balance_loss(const moe_config* cfg, const moe_router* router, con
                             size_t workspace_bytes, void* stream);
 
 /*
+ * moe_forward with moe_route_scored's routing (bias may be NULL).
+ */
+moe_status moe_forward_scored(const moe_config* cfg, const moe_router* router, const moe_weights* w,
+                              const void* w_router, const float* bias, const void* x, void* y,
+                              int32_t xy_on_host, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * moe_backward for a layer routed by moe_route_scored: dlogits, dx and dw_router hold
+ * moe_route_backward's gradient, with the balance loss's where dscore is given (dscore,
+ * seq_offsets, n_seq and dloss as there).
+ */
+moe_status moe_backward_scored(const moe_config* cfg, const moe_router* router,
+                               const moe_weights* w, const moe_bwd_weights* wb,
+                               const moe_fwd_saved* saved, const void* dy, void* dx,
+                               float* dlogits, float* dgate, const float* dscore,
+                               const int32_t* seq_offsets, int32_t n_seq, const float* dloss,
+                               const moe_weight_grads* dw, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
  * Orthogonalised updates (the Muon optimiser's, for the weight gradients moe_backward
  * writes): each of `groups` stacked row-major matrices [rows, cols] is divided by its
  * Frobenius norm + eps and taken through `steps` steps of

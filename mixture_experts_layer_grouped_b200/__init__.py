@@ -48,4 +48,5 @@ from .binding import (  # noqa: F401
     moe_muon_workspace_size,
     moe_orthogonalize,
     moe_muon_step,
+    MoEMuon,
 )

@@ -158,6 +158,13 @@ def lib() -> ctypes.CDLL:
                                   ctypes.c_size_t, _VP], ctypes.c_int),
             "moe_route_backward": ([_CFG, _RTR, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP,
                                     _VP, _VP], ctypes.c_int),
+            "moe_forward_scored": ([_CFG, _RTR, ctypes.POINTER(MoEWeights), _VP, _VP, _VP, _VP,
+                                    ctypes.c_int32, _VP, ctypes.c_size_t, _VP], ctypes.c_int),
+            "moe_backward_scored": ([_CFG, _RTR, ctypes.POINTER(MoEWeights),
+                                     ctypes.POINTER(MoEBwdWeights), ctypes.POINTER(MoEFwdSaved),
+                                     _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP,
+                                     ctypes.POINTER(MoEWeightGrads), _VP, ctypes.c_size_t, _VP],
+                                    ctypes.c_int),
             "moe_balance_workspace_size": ([_CFG, ctypes.c_int32,
                                             ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
             "moe_balance_loss": ([_CFG, _RTR, _VP, _VP, _VP, ctypes.c_int32, ctypes.c_float, _VP,
@@ -348,16 +355,21 @@ def moe_combine(cfg, out_rows, token_row, topk_w, y, shared_out=None, stream=Non
         _p(_cuda(shared_out, bf, "shared_out")), _p(_cuda(y, bf, "y")), _stream(stream)))
 
 
-def moe_forward(cfg, weights, w_router, bias, x, y, workspace, stream=None):
-    """Whole layer.  If x and y are host tensors they are copied inside the call."""
+def moe_forward(cfg, weights, w_router, bias, x, y, workspace, stream=None, router=None):
+    """Whole layer.  If x and y are host tensors they are copied inside the call.  With
+    ``router`` (an MoERouter; bias may then be None) it is moe_forward_scored."""
     ws = weights if isinstance(weights, MoEWeights) else weights_struct(weights)
     on_host = not x.is_cuda
     if on_host != (not y.is_cuda):
         raise ValueError("x and y must both be host tensors or both device tensors")
-    _check("moe_forward", lib().moe_forward(
-        ctypes.byref(cfg), ctypes.byref(ws), _p(_cuda(w_router, torch.bfloat16, "w_router")),
-        _p(_cuda(bias, torch.float32, "bias")), _p(x), _p(y), 1 if on_host else 0,
-        _p(workspace), workspace.numel(), _stream(stream)))
+    rest = (ctypes.byref(ws), _p(_cuda(w_router, torch.bfloat16, "w_router")),
+            _p(_cuda(bias, torch.float32, "bias")), _p(x), _p(y), 1 if on_host else 0,
+            _p(workspace), workspace.numel(), _stream(stream))
+    if router is None:
+        _check("moe_forward", lib().moe_forward(ctypes.byref(cfg), *rest))
+    else:
+        _check("moe_forward_scored",
+               lib().moe_forward_scored(ctypes.byref(cfg), ctypes.byref(router), *rest))
 
 
 def moe_get_device_status(workspace, stream=None) -> int:
@@ -411,12 +423,14 @@ def moe_backward_workspace_size(cfg: MoEConfig) -> int:
 
 
 def moe_backward(cfg, weights, bwd_weights, saved: dict, dy, dx, workspace, dlogits=None,
-                 dgate=None, grads=None, accumulate=False, stream=None):
+                 dgate=None, grads=None, accumulate=False, stream=None, router=None, dscore=None,
+                 seq_offsets=None, dloss=None):
     """Gradients of the bf16 layer.  ``saved`` maps the moe_fwd_saved field
     names (x, rows, logits, topk_idx, topk_w, counts, offsets, row_token,
     token_row, out_rows) to the forward's tensors; ``grads`` (optional) maps
     dw1, dw3, dw2, dws1, dws3, dws2, dw_router to fp32 output tensors, which
-    are overwritten, or added to with ``accumulate=True``."""
+    are overwritten, or added to with ``accumulate=True``.  With ``router`` it is
+    moe_backward_scored (``dscore``, ``seq_offsets``, ``dloss`` as in moe_route_backward)."""
     ws = weights if isinstance(weights, MoEWeights) else weights_struct(weights)
     bw = bwd_weights if isinstance(bwd_weights, MoEBwdWeights) else MoEBwdWeights(
         **{k: (bwd_weights[k].data_ptr() if bwd_weights.get(k) is not None else None)
@@ -431,13 +445,20 @@ def moe_backward(cfg, weights, bwd_weights, saved: dict, dy, dx, workspace, dlog
         gr = MoEWeightGrads(**{k: (_cuda(grads[k], torch.float32, k).data_ptr()
                                    if grads.get(k) is not None else None)
                                for k in _GRAD_FIELDS}, accumulate=1 if accumulate else 0)
-    bf = torch.bfloat16
-    _check("moe_backward", lib().moe_backward(
-        ctypes.byref(cfg), ctypes.byref(ws), ctypes.byref(bw), ctypes.byref(sv),
-        _p(_cuda(dy, bf, "dy")), _p(_cuda(dx, bf, "dx")),
-        _p(_cuda(dlogits, torch.float32, "dlogits")), _p(_cuda(dgate, torch.float32, "dgate")),
-        ctypes.byref(gr) if gr is not None else None, _p(workspace), workspace.numel(),
-        _stream(stream)))
+    bf, f32 = torch.bfloat16, torch.float32
+    first = (ctypes.byref(ws), ctypes.byref(bw), ctypes.byref(sv), _p(_cuda(dy, bf, "dy")),
+             _p(_cuda(dx, bf, "dx")), _p(_cuda(dlogits, f32, "dlogits")),
+             _p(_cuda(dgate, f32, "dgate")))
+    last = (ctypes.byref(gr) if gr is not None else None, _p(workspace), workspace.numel(),
+            _stream(stream))
+    if router is None:
+        _check("moe_backward", lib().moe_backward(ctypes.byref(cfg), *first, *last))
+        return
+    off, n_seq = _sequences(seq_offsets)
+    _check("moe_backward_scored", lib().moe_backward_scored(
+        ctypes.byref(cfg), ctypes.byref(router), *first,
+        _sized(dscore, f32, (n_seq, cfg.E), "dscore"), off, n_seq, _p(_cuda(dloss, f32, "dloss")),
+        *last))
 
 
 def _sized(t, dtype, shape, name):
@@ -554,12 +575,14 @@ class MoELayer:
     ``weights`` maps the moe_weights field names (w1, w3, w2, ws1, ...) to
     row-major bf16 device tensors, which are prepared once into the kernels'
     layout (or to already prepared buffers with ``prepared=True``);
-    ``forward(x)`` runs the whole layer through moe_forward.
+    ``forward(x)`` runs the whole layer through moe_forward, or with ``router`` (an
+    MoERouter; bias may then be None) through moe_forward_scored.
     """
 
     def __init__(self, cfg: MoEConfig, weights: dict, w_router, bias, device="cuda",
-                 prepared=False):
+                 prepared=False, router=None):
         self.cfg = cfg
+        self.router = router
         self.weights = dict(weights) if prepared else prepare_weights(cfg, weights)
         self._ws_struct = weights_struct(self.weights)
         self.w_router = w_router
@@ -571,7 +594,7 @@ class MoELayer:
             out = torch.empty(self.cfg.T, self.cfg.H, dtype=torch.bfloat16, device=x.device,
                               pin_memory=not x.is_cuda)
         moe_forward(self.cfg, self._ws_struct, self.w_router, self.bias, x, out, self.workspace,
-                    stream)
+                    stream, router=self.router)
         return out
 
     def device_status(self) -> int:
@@ -589,10 +612,22 @@ class MoETrainLayer(MoELayer):
     forward and transposed for the backward once, here.  Routed weight
     gradients need cfg.pad_multiple % 64 == 0.  The forward keeps x by
     reference: it must not change before the backward that follows.
+
+    With ``router`` (an MoERouter) the layer is routed by moe_route_scored.  A
+    ``balance_coef`` above 0 then adds the balance loss over the sequences that
+    ``forward(x, seq_offsets)`` names (one by default): the forward leaves it and
+    each sequence's expert loads in ``balance["loss"]`` and ``balance["load"]``, and
+    the backward includes its gradient (that of y's loss plus this one).
     """
 
-    def __init__(self, cfg: MoEConfig, weights: dict, w_router, bias, device="cuda"):
-        super().__init__(cfg, weights, w_router, bias, device)
+    def __init__(self, cfg: MoEConfig, weights: dict, w_router, bias, device="cuda",
+                 router=None, balance_coef=0.0):
+        super().__init__(cfg, weights, w_router, bias, device, router=router)
+        if balance_coef and router is None:
+            raise ValueError("balance_coef needs a router (MoERouter)")
+        self.balance_coef = balance_coef
+        self.balance = None
+        self.seq_offsets = None
         self.bwd_weights = prepare_backward_weights(cfg, weights, w_router)
         nbytes, r_cap = moe_workspace_size(cfg)
         self.step_ws = new_workspace(nbytes, device)
@@ -610,12 +645,48 @@ class MoETrainLayer(MoELayer):
         self.shared_out = (torch.empty(T, H, dtype=torch.bfloat16, device=device)
                            if cfg.I_shared > 0 else None)
 
-    def forward(self, x, out=None, stream=None):
+    def _balance_buffers(self, n_seq):
+        if self.balance is None or self.balance["load"].shape[0] != n_seq:
+            c, dev = self.cfg, self.saved["logits"].device
+            self.balance = {
+                "loss": torch.empty(1, dtype=torch.float32, device=dev),
+                "load": torch.empty(n_seq, c.E, dtype=torch.int32, device=dev),
+                "dscore": torch.empty(n_seq, c.E, dtype=torch.float32, device=dev),
+                "workspace": new_workspace(moe_balance_workspace_size(c, n_seq), dev)}
+        return self.balance
+
+    def update_weights(self, weights: dict, w_router, stream=None):
+        """Prepare new values of the row-major weights and the router weight into the layer's
+        own buffers (after an optimiser's step)."""
+        c = self.cfg
+        moe_prepare_weights(c, 0, 0, c.E, weights["w1"], weights["w3"], weights["w2"],
+                            self._ws_struct, stream)
+        if c.I_shared > 0:
+            moe_prepare_weights(c, 1, 0, 1, weights["ws1"], weights["ws3"], weights["ws2"],
+                                self._ws_struct, stream)
+        moe_prepare_backward_weights(c, 0, 0, c.E, weights["w1"], weights["w3"], weights["w2"],
+                                     None, self.bwd_weights, stream)
+        moe_prepare_backward_weights(c, 1, 0, 1, weights.get("ws1"), weights.get("ws3"),
+                                     weights.get("ws2"), w_router, self.bwd_weights, stream)
+        self.w_router = w_router
+
+    def forward(self, x, out=None, stream=None, seq_offsets=None):
         c, sv = self.cfg, self.saved
         if out is None:
             out = torch.empty(c.T, c.H, dtype=torch.bfloat16, device=x.device)
-        moe_route(c, x, self.w_router, self.bias, sv["topk_idx"], sv["topk_w"], self.step_ws,
-                  logits_out=sv["logits"], stream=stream)
+        if self.router is None:
+            moe_route(c, x, self.w_router, self.bias, sv["topk_idx"], sv["topk_w"], self.step_ws,
+                      logits_out=sv["logits"], stream=stream)
+        else:
+            moe_route_scored(c, self.router, sv["topk_idx"], sv["topk_w"], x=x,
+                             w_router=self.w_router, bias=self.bias, workspace=self.step_ws,
+                             logits_out=sv["logits"], stream=stream)
+        if self.balance_coef:
+            self.seq_offsets = seq_offsets
+            b = self._balance_buffers(1 if seq_offsets is None else seq_offsets.numel() - 1)
+            moe_balance_loss(c, self.router, sv["logits"], sv["topk_idx"], self.balance_coef,
+                             b["loss"], b["load"], b["dscore"], b["workspace"],
+                             seq_offsets=seq_offsets, stream=stream)
         moe_permute(c, sv["topk_idx"], x, sv["counts"], sv["offsets"], sv["row_token"],
                     sv["token_row"], sv["rows"], self.step_ws, stream=stream)
         moe_grouped_mlp(c, self._ws_struct, sv["rows"], sv["counts"], sv["offsets"],
@@ -650,8 +721,50 @@ class MoETrainLayer(MoELayer):
             res.update(grads)
         moe_backward(c, self._ws_struct, self.bwd_weights, self.saved, dy, dx, self.bwd_ws,
                      dlogits=res["dlogits"], dgate=res["dgate"], grads=grads,
-                     accumulate=accumulate, stream=stream)
+                     accumulate=accumulate, stream=stream, router=self.router,
+                     dscore=self.balance["dscore"] if self.balance_coef else None,
+                     seq_offsets=self.seq_offsets)
         return res
 
     def device_status(self) -> int:
         return max(moe_get_device_status(self.step_ws), moe_get_device_status(self.bwd_ws))
+
+
+class MoEMuon:
+    """Muon for a layer's row-major bf16 weights, updated in place.
+
+    ``weights`` maps names to tensors [groups, rows, cols] or [rows, cols] (each stacked
+    matrix is orthogonalised by itself: one expert's weight); the momentum of each is kept
+    here in fp32.  ``step(grads, lr)`` takes gradients keyed like moe_weight_grads ("d" and
+    the weight's name; fp32 or bf16); a weight without one is left as it is.  The update of a
+    matrix is lr * sqrt(max(1, rows / cols)) times the orthogonalised one, and lr * decay of
+    the weight is taken off.
+    """
+
+    def __init__(self, weights: dict, beta=0.95, nesterov=True, decay=0.0, steps=5,
+                 coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7):
+        self.weights = weights
+        self.beta, self.nesterov, self.decay = beta, nesterov, decay
+        self.configs, self.momentum = {}, {}
+        a, b, c = coefficients
+        size = 0
+        for name, w in weights.items():
+            groups = w.shape[0] if w.dim() == 3 else 1
+            self.configs[name] = MoEMuonConfig(groups=groups, rows=w.shape[-2], cols=w.shape[-1],
+                                               steps=steps, a=a, b=b, c=c, eps=eps)
+            self.momentum[name] = torch.zeros_like(w, dtype=torch.float32)
+            size = max(size, moe_muon_workspace_size(self.configs[name]))
+        self.workspace = new_workspace(size, next(iter(weights.values())).device)
+
+    def step(self, grads: dict, lr, stream=None):
+        for name, w in self.weights.items():
+            g = grads.get("d" + name)
+            if g is None:
+                continue
+            c, m = self.configs[name], self.momentum[name]
+            moe_muon_step(c, g, m, m, w, w, self.workspace, beta=self.beta,
+                          nesterov=self.nesterov, step=lr * max(1.0, c.rows / c.cols) ** 0.5,
+                          decay=lr * self.decay, stream=stream)
+
+    def device_status(self) -> int:
+        return moe_get_device_status(self.workspace)

@@ -26,7 +26,7 @@ struct CombineBwdArgs {
   const int32_t* token_row;       // [T * k]
   const int32_t* topk_idx;        // [T * k]
   const float* topk_w;            // [T * k]
-  const float* logits;            // [T, E]: the forward's router logits
+  const float* logits;            // [T, E]: the forward's router logits; null: no gate backward here
   __nv_bfloat16* dO;              // [r_cap, H]
   float* dgate;                   // [T * k]
   float* dlogits;                 // [T, E] or null
@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBwdArgs a)
 #pragma unroll
   for (int j = 0; j < KM; ++j)
     if (j < kk && lane == j) a.dgate[static_cast<int64_t>(t) * kk + j] = part[j];
+  if (!a.logits) return;  // the scored router's gates: route_backward_kernel
   // gate backward: the token's dlogits (fp32, optional) and their bf16 copy in
   // the dense GEMM's operand row, zeros elsewhere
   const float* lg = a.logits + static_cast<int64_t>(t) * a.E;

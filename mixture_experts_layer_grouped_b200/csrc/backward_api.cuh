@@ -186,9 +186,10 @@ bool wants_routed_wgrad(const moe_weight_grads* dw) {
 }
 
 template <int TILE_N, bool PAIR>
-moe_status backward_steps(const moe_config& c, const moe_weights& w, const moe_bwd_weights& wb,
-                          const moe_fwd_saved& f, const void* dy, void* dx, float* dlogits,
-                          float* dgate, const moe_weight_grads* dw, void* ws, cudaStream_t s) {
+moe_status backward_steps(const moe_config& c, const moe_router* router, const BalanceGrad& bal,
+                          const moe_weights& w, const moe_bwd_weights& wb, const moe_fwd_saved& f,
+                          const void* dy, void* dx, float* dlogits, float* dgate,
+                          const moe_weight_grads* dw, void* ws, cudaStream_t s) {
   const BwdLayout L = bwd_layout(c);
   uint8_t* b = static_cast<uint8_t*>(ws);
   int32_t* status = status_ptr(ws);
@@ -204,7 +205,7 @@ moe_status backward_steps(const moe_config& c, const moe_weights& w, const moe_b
   cb.token_row = f.token_row;
   cb.topk_idx = f.topk_idx;
   cb.topk_w = f.topk_w;
-  cb.logits = f.logits;
+  cb.logits = router ? nullptr : f.logits;  // a scored router's gradient follows by itself
   cb.dO = bfp(L.dO);
   cb.dgate = dgate ? dgate : reinterpret_cast<float*>(b + L.dgate);
   cb.dlogits = dlogits;
@@ -229,6 +230,9 @@ moe_status backward_steps(const moe_config& c, const moe_weights& w, const moe_b
     default: MOE_TRY(launch_pdl(combine_backward_kernel<0>, cgrid, dim3(256), 0, s, cb)); break;
   }
   MOE_TRY(launch_check());
+  if (router)
+    MOE_TRY(do_route_backward(c, *router, f.logits, f.topk_idx, cb.dgate, bal, dlogits, cb.dense_b,
+                              cb.col_b, cb.ld_b, s));
   const unsigned g = static_cast<unsigned>(sm_count() * 8);
   if (wants_routed_wgrad(dw)) {
     // dO^T h contracts over the pad rows too: they must hold zeros
@@ -303,6 +307,26 @@ moe_status check_bwd(const moe_config& c, const moe_weights* w, const moe_bwd_we
       if (q && !aligned16(q)) return MOE_ERR_INVALID_ARG;
   }
   return MOE_OK;
+}
+
+// router null: moe_route's gates.
+moe_status backward_layer(const moe_config* cfg, const moe_router* router, const BalanceGrad& bal,
+                          const moe_weights* w, const moe_bwd_weights* wb,
+                          const moe_fwd_saved* saved, const void* dy, void* dx, float* dlogits,
+                          float* dgate, const moe_weight_grads* dw, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  MOE_TRY(check_config(cfg));
+  const moe_config& c = *cfg;
+  MOE_TRY(check_bwd(c, w, wb, saved, dy, dx, dw));
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < bwd_layout(c).total) return MOE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // tiles as the forward's bf16 grouped GEMMs pick them
+  const bool small = static_cast<int64_t>(c.T) * c.top_k <= 32LL * c.E;
+  const bool pairs = !small && use_pairs(c, saved->rows);
+  auto steps = small ? backward_steps<64, false>
+                     : (pairs ? backward_steps<256, true> : backward_steps<256, false>);
+  return steps(c, router, bal, *w, *wb, *saved, dy, dx, dlogits, dgate, dw, workspace, s);
 }
 
 }  // namespace
@@ -405,19 +429,22 @@ moe_status moe_backward(const moe_config* cfg, const moe_weights* w, const moe_b
                         const moe_fwd_saved* saved, const void* dy, void* dx, float* dlogits,
                         float* dgate, const moe_weight_grads* dw, void* workspace,
                         size_t workspace_bytes, void* stream) {
-  MOE_TRY(check_config(cfg));
-  const moe_config& c = *cfg;
-  MOE_TRY(check_bwd(c, w, wb, saved, dy, dx, dw));
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign) return MOE_ERR_INVALID_ARG;
-  if (workspace_bytes < bwd_layout(c).total) return MOE_ERR_WORKSPACE;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // tiles as the forward's bf16 grouped GEMMs pick them
-  const bool small = static_cast<int64_t>(c.T) * c.top_k <= 32LL * c.E;
-  if (small)
-    return backward_steps<64, false>(c, *w, *wb, *saved, dy, dx, dlogits, dgate, dw, workspace, s);
-  if (use_pairs(c, saved->rows))
-    return backward_steps<256, true>(c, *w, *wb, *saved, dy, dx, dlogits, dgate, dw, workspace, s);
-  return backward_steps<256, false>(c, *w, *wb, *saved, dy, dx, dlogits, dgate, dw, workspace, s);
+  return backward_layer(cfg, nullptr, BalanceGrad{}, w, wb, saved, dy, dx, dlogits, dgate, dw,
+                        workspace, workspace_bytes, stream);
+}
+
+moe_status moe_backward_scored(const moe_config* cfg, const moe_router* router,
+                               const moe_weights* w, const moe_bwd_weights* wb,
+                               const moe_fwd_saved* saved, const void* dy, void* dx,
+                               float* dlogits, float* dgate, const float* dscore,
+                               const int32_t* seq_offsets, int32_t n_seq, const float* dloss,
+                               const moe_weight_grads* dw, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  MOE_TRY(check_router(router));
+  const BalanceGrad bal{dscore, seq_offsets, n_seq, dloss};
+  MOE_TRY(check_balance_grad(bal));
+  return backward_layer(cfg, router, bal, w, wb, saved, dy, dx, dlogits, dgate, dw, workspace,
+                        workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -869,6 +869,114 @@ moe_status check_weights(const moe_config& c, const moe_weights* w) {
   return MOE_OK;
 }
 
+moe_status do_route_scored(const moe_config& c, const moe_router& r, const void* x,
+                           const void* w_router, const float* bias, const float* logits_in,
+                           float* logits_out, int32_t* topk_idx, float* topk_w, void* ws,
+                           cudaStream_t s);
+
+// The whole layer; router null: moe_route's form.
+moe_status forward_layer(const moe_config* cfg, const moe_router* router, const moe_weights* w,
+                         const void* w_router, const float* bias, const void* x, void* y,
+                         int32_t xy_on_host, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  MOE_TRY(check_config(cfg));
+  MOE_TRY(check_dtype(cfg));
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign) return MOE_ERR_INVALID_ARG;
+  const FwdLayout F = fwd_layout(*cfg);
+  if (workspace_bytes < F.total) return MOE_ERR_WORKSPACE;
+  MOE_TRY(check_weights(*cfg, w));
+  if (!w_router || (!bias && !router) || !x || !y || !aligned16(w_router))
+    return MOE_ERR_INVALID_ARG;
+  const moe_config& c = *cfg;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* b = static_cast<uint8_t*>(workspace);
+  const size_t xbytes = static_cast<size_t>(c.T) * c.H * 2;
+  const void* xd = x;
+  void* yd = y;
+  if (xy_on_host) {
+    MOE_CUDA(cudaMemcpyAsync(b + F.x, x, xbytes, cudaMemcpyHostToDevice, s));
+    xd = b + F.x;
+    yd = b + F.y;
+  } else if (!aligned16(x) || !aligned16(y)) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  float* logits = reinterpret_cast<float*>(b + F.logits);
+  int32_t* topk_idx = reinterpret_cast<int32_t*>(b + F.topk_idx);
+  float* topk_w = reinterpret_cast<float*>(b + F.topk_w);
+  int32_t* counts = reinterpret_cast<int32_t*>(b + F.counts);
+  int32_t* offsets = reinterpret_cast<int32_t*>(b + F.offsets);
+  int32_t* row_token = reinterpret_cast<int32_t*>(b + F.row_token);
+  int32_t* token_row = reinterpret_cast<int32_t*>(b + F.token_row);
+  void* out_rows = b + F.out_rows;
+  void* shared_out = c.I_shared > 0 ? b + F.shared_out : nullptr;
+  MOE_TRY(zero_mlp_scratch(c, workspace, s));
+  if (router)
+    MOE_TRY(do_route_scored(c, *router, xd, w_router, bias, nullptr, logits, topk_idx, topk_w,
+                            workspace, s));
+  else
+    MOE_TRY(do_route(c, xd, w_router, bias, nullptr, logits, topk_idx, topk_w, workspace, s));
+  // an expert-major copy of the rows: fc1 reads it with 32-row TMA boxes, which
+  // streams faster than per-row gathers from x (moe_grouped_mlp with rows == NULL)
+  void* rows = b + F.rows;
+  const void* xq = xd;
+  MlpQuant q{nullptr, nullptr, nullptr, nullptr};
+  if (is_bf16(c)) {
+    MOE_TRY(do_permute(c, topk_idx, xd, nullptr, counts, offsets, row_token, token_row, rows,
+                       nullptr, workspace, s));
+  } else if (is_mx(c)) {
+    // MXFP8: quantize in token order, then gather codes and scales (its top_k
+    // row copies make the one-pass form below write-bound and slower on B200:
+    // DeepSeek-V3 dims 103 us against 15 + 73 us)
+    float* xg = reinterpret_cast<float*>(b + F.x_g);
+    MOE_TRY(moe_quantize(c.dtype, xd, c.T, c.H, b + F.x_q, b + F.x_sf, xg, s));
+    xq = b + F.x_q;
+    q = MlpQuant{b + F.rows_sf, b + F.x_sf, xg, nullptr};
+    MOE_TRY(do_permute(c, topk_idx, xq, q.x_scales, counts, offsets, row_token, token_row, rows,
+                       b + F.rows_sf, workspace, s));
+  } else {
+    // NVFP4: each token is quantized once and its codes and scales go straight
+    // to its expert-major rows (and to token order for the shared expert),
+    // after x's global scale is taken from its amax
+    float* xg = reinterpret_cast<float*>(b + F.x_g);
+    {
+      const int64_t n = static_cast<int64_t>(c.T) * c.H;
+      MOE_CUDA(cudaMemsetAsync(xg, 0, 4, s));
+      const unsigned nb = static_cast<unsigned>((n / 8 + 255) / 256 < 2048 ? (n / 8 + 255) / 256 : 2048);
+      MOE_TRY(launch_pdl(amax_groups_kernel, dim3(nb, 1), dim3(256), 0, s,
+                         static_cast<const __nv_bfloat16*>(xd), n, xg));
+      MOE_TRY(launch_check());
+      MOE_TRY(launch_pdl(amax_to_global_kernel, dim3(1), dim3(32), 0, s, xg, 1));
+      MOE_TRY(launch_check());
+    }
+    MOE_TRY(do_permute_maps(c, topk_idx, counts, offsets, row_token, token_row, workspace, s));
+    const bool sh = c.I_shared > 0;
+    QScatterArgs qa;
+    qa.x = static_cast<const __nv_bfloat16*>(xd);
+    qa.token_row = token_row;
+    qa.row_token = row_token;
+    qa.offsets = offsets;
+    qa.rows = static_cast<uint8_t*>(rows);
+    qa.rows_sf = b + F.rows_sf;
+    qa.xq = sh ? b + F.x_q : nullptr;
+    qa.xq_sf = sh ? b + F.x_sf : nullptr;
+    qa.g = xg;
+    qa.T = c.T;
+    qa.H = c.H;
+    qa.k = c.top_k;
+    qa.E = c.E;
+    const dim3 grid(sm_count() * 8), block(256);
+    MOE_TRY(launch_pdl(quantize_scatter_nvfp4_kernel, grid, block, 0, s, qa));
+    MOE_TRY(launch_check());
+    xq = b + F.x_q;
+    q = MlpQuant{b + F.rows_sf, b + F.x_sf, xg, nullptr};
+  }
+  MOE_TRY(do_grouped_mlp(c, *w, rows, xq, q, counts, offsets, out_rows, shared_out, workspace,
+                         s, /*scratch_zeroed=*/true));
+  MOE_TRY(do_combine(c, out_rows, token_row, topk_w, shared_out, yd, s));
+  if (xy_on_host) MOE_CUDA(cudaMemcpyAsync(y, yd, xbytes, cudaMemcpyDeviceToHost, s));
+  return MOE_OK;
+}
+
 }  // namespace
 
 // ===========================================================================
@@ -1146,97 +1254,8 @@ moe_status moe_forward_workspace_size(const moe_config* cfg, size_t* bytes) {
 moe_status moe_forward(const moe_config* cfg, const moe_weights* w, const void* w_router,
                        const float* bias, const void* x, void* y, int32_t xy_on_host,
                        void* workspace, size_t workspace_bytes, void* stream) {
-  MOE_TRY(check_config(cfg));
-  MOE_TRY(check_dtype(cfg));
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign) return MOE_ERR_INVALID_ARG;
-  const FwdLayout F = fwd_layout(*cfg);
-  if (workspace_bytes < F.total) return MOE_ERR_WORKSPACE;
-  MOE_TRY(check_weights(*cfg, w));
-  if (!w_router || !bias || !x || !y || !aligned16(w_router)) return MOE_ERR_INVALID_ARG;
-  const moe_config& c = *cfg;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint8_t* b = static_cast<uint8_t*>(workspace);
-  const size_t xbytes = static_cast<size_t>(c.T) * c.H * 2;
-  const void* xd = x;
-  void* yd = y;
-  if (xy_on_host) {
-    MOE_CUDA(cudaMemcpyAsync(b + F.x, x, xbytes, cudaMemcpyHostToDevice, s));
-    xd = b + F.x;
-    yd = b + F.y;
-  } else if (!aligned16(x) || !aligned16(y)) {
-    return MOE_ERR_INVALID_ARG;
-  }
-  float* logits = reinterpret_cast<float*>(b + F.logits);
-  int32_t* topk_idx = reinterpret_cast<int32_t*>(b + F.topk_idx);
-  float* topk_w = reinterpret_cast<float*>(b + F.topk_w);
-  int32_t* counts = reinterpret_cast<int32_t*>(b + F.counts);
-  int32_t* offsets = reinterpret_cast<int32_t*>(b + F.offsets);
-  int32_t* row_token = reinterpret_cast<int32_t*>(b + F.row_token);
-  int32_t* token_row = reinterpret_cast<int32_t*>(b + F.token_row);
-  void* out_rows = b + F.out_rows;
-  void* shared_out = c.I_shared > 0 ? b + F.shared_out : nullptr;
-  MOE_TRY(zero_mlp_scratch(c, workspace, s));
-  MOE_TRY(do_route(c, xd, w_router, bias, nullptr, logits, topk_idx, topk_w, workspace, s));
-  // an expert-major copy of the rows: fc1 reads it with 32-row TMA boxes, which
-  // streams faster than per-row gathers from x (moe_grouped_mlp with rows == NULL)
-  void* rows = b + F.rows;
-  const void* xq = xd;
-  MlpQuant q{nullptr, nullptr, nullptr, nullptr};
-  if (is_bf16(c)) {
-    MOE_TRY(do_permute(c, topk_idx, xd, nullptr, counts, offsets, row_token, token_row, rows,
-                       nullptr, workspace, s));
-  } else if (is_mx(c)) {
-    // MXFP8: quantize in token order, then gather codes and scales (its top_k
-    // row copies make the one-pass form below write-bound and slower on B200:
-    // DeepSeek-V3 dims 103 us against 15 + 73 us)
-    float* xg = reinterpret_cast<float*>(b + F.x_g);
-    MOE_TRY(moe_quantize(c.dtype, xd, c.T, c.H, b + F.x_q, b + F.x_sf, xg, s));
-    xq = b + F.x_q;
-    q = MlpQuant{b + F.rows_sf, b + F.x_sf, xg, nullptr};
-    MOE_TRY(do_permute(c, topk_idx, xq, q.x_scales, counts, offsets, row_token, token_row, rows,
-                       b + F.rows_sf, workspace, s));
-  } else {
-    // NVFP4: each token is quantized once and its codes and scales go straight
-    // to its expert-major rows (and to token order for the shared expert),
-    // after x's global scale is taken from its amax
-    float* xg = reinterpret_cast<float*>(b + F.x_g);
-    {
-      const int64_t n = static_cast<int64_t>(c.T) * c.H;
-      MOE_CUDA(cudaMemsetAsync(xg, 0, 4, s));
-      const unsigned nb = static_cast<unsigned>((n / 8 + 255) / 256 < 2048 ? (n / 8 + 255) / 256 : 2048);
-      MOE_TRY(launch_pdl(amax_groups_kernel, dim3(nb, 1), dim3(256), 0, s,
-                         static_cast<const __nv_bfloat16*>(xd), n, xg));
-      MOE_TRY(launch_check());
-      MOE_TRY(launch_pdl(amax_to_global_kernel, dim3(1), dim3(32), 0, s, xg, 1));
-      MOE_TRY(launch_check());
-    }
-    MOE_TRY(do_permute_maps(c, topk_idx, counts, offsets, row_token, token_row, workspace, s));
-    const bool sh = c.I_shared > 0;
-    QScatterArgs qa;
-    qa.x = static_cast<const __nv_bfloat16*>(xd);
-    qa.token_row = token_row;
-    qa.row_token = row_token;
-    qa.offsets = offsets;
-    qa.rows = static_cast<uint8_t*>(rows);
-    qa.rows_sf = b + F.rows_sf;
-    qa.xq = sh ? b + F.x_q : nullptr;
-    qa.xq_sf = sh ? b + F.x_sf : nullptr;
-    qa.g = xg;
-    qa.T = c.T;
-    qa.H = c.H;
-    qa.k = c.top_k;
-    qa.E = c.E;
-    const dim3 grid(sm_count() * 8), block(256);
-    MOE_TRY(launch_pdl(quantize_scatter_nvfp4_kernel, grid, block, 0, s, qa));
-    MOE_TRY(launch_check());
-    xq = b + F.x_q;
-    q = MlpQuant{b + F.rows_sf, b + F.x_sf, xg, nullptr};
-  }
-  MOE_TRY(do_grouped_mlp(c, *w, rows, xq, q, counts, offsets, out_rows, shared_out, workspace,
-                         s, /*scratch_zeroed=*/true));
-  MOE_TRY(do_combine(c, out_rows, token_row, topk_w, shared_out, yd, s));
-  if (xy_on_host) MOE_CUDA(cudaMemcpyAsync(y, yd, xbytes, cudaMemcpyDeviceToHost, s));
-  return MOE_OK;
+  return forward_layer(cfg, nullptr, w, w_router, bias, x, y, xy_on_host, workspace,
+                       workspace_bytes, stream);
 }
 
 moe_status moe_get_device_status(void* workspace, int32_t* device_status, void* stream) {
@@ -1380,9 +1399,11 @@ extern "C" moe_status moe_permute_noalloc(const moe_config* cfg, const int32_t* 
   return launch_check();
 }
 
+// The scored router, its gradient and the balance loss.
+#include "route_scored_api.cuh"
+
 // The backward of the bf16 layer: its host steps and its C ABI.
 #include "backward_api.cuh"
 
-// The scored router with its gradient and the balance loss, and the orthogonalised updates.
-#include "route_scored_api.cuh"
+// The orthogonalised updates.
 #include "muon_api.cuh"

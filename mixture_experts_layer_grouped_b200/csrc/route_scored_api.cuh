@@ -151,6 +151,15 @@ moe_status moe_route_scored(const moe_config* cfg, const moe_router* router, con
                          workspace, static_cast<cudaStream_t>(stream));
 }
 
+moe_status moe_forward_scored(const moe_config* cfg, const moe_router* router, const moe_weights* w,
+                              const void* w_router, const float* bias, const void* x, void* y,
+                              int32_t xy_on_host, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  MOE_TRY(check_router(router));
+  return forward_layer(cfg, router, w, w_router, bias, x, y, xy_on_host, workspace,
+                       workspace_bytes, stream);
+}
+
 moe_status moe_route_backward(const moe_config* cfg, const moe_router* router, const float* logits,
                               const int32_t* topk_idx, const float* dgate, const float* dscore,
                               const int32_t* seq_offsets, int32_t n_seq, const float* dloss,
