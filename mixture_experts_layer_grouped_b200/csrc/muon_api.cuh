@@ -75,17 +75,19 @@ moe_status check_muon(const moe_muon_config* c) {
   return MOE_OK;
 }
 
-// [groups, rows, inner] fp16 with row length ld: boxes of 64 elements x box_rows rows.
+// [groups, rows, inner] of 16-bit elements with row length ld: boxes of box_cols x box_rows,
+// swizzled over the 128 or 64 bytes of a box row.
 moe_status make_ns_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
-                       uint64_t groups, uint64_t ld, uint32_t box_rows) {
+                       uint64_t groups, uint64_t ld, uint32_t box_rows, uint32_t box_cols) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return MOE_ERR_CUDA;
   cuuint64_t dims[3] = {inner, rows, groups};
   cuuint64_t strides[2] = {ld * 2, rows * ld * 2};
-  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     fprintf(stderr, "moe_b200: cuTensorMapEncodeTiled (muon) failed (%d)\n", static_cast<int>(r));
@@ -94,10 +96,11 @@ moe_status make_ns_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_
   return MOE_OK;
 }
 
-template <int MODE, bool A_MN, bool B_MN, bool PAIR, bool LAST>
+template <int MODE, bool TALL, bool PAIR, bool LAST>
 moe_status launch_ns(const NsParams& p, cudaStream_t s) {
-  auto kern = ns_gemm_kernel<MODE, A_MN, B_MN, PAIR, LAST>;
-  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmemBytes));
+  auto kern = ns_gemm_kernel<MODE, TALL, PAIR, LAST>;
+  constexpr int smem = NsCfg<MODE, PAIR, LAST>::SMEM_BYTES;
+  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   int ctas = sm_count() / (PAIR ? 2 : 1);
   if (p.total < ctas) ctas = p.total;
   cudaLaunchConfig_t cfg = {};
@@ -117,7 +120,7 @@ moe_status launch_ns(const NsParams& p, cudaStream_t s) {
   }
   cfg.gridDim = dim3(PAIR ? 2 * ctas : ctas);
   cfg.blockDim = dim3(kNsThreads);
-  cfg.dynamicSmemBytes = kNsSmemBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = n;
@@ -149,89 +152,106 @@ moe_status ns_steps(const moe_muon_config& c, const MuonArgs& u, const MuonLayou
   auto half_at = [&](size_t off) { return reinterpret_cast<__half*>(b + off); };
   auto tiles = [](int n) { return (n + TILE - 1) / TILE; };
   const int rt = tiles(r);
+  // maps of the working copies: X[buffer][hi, lo], A and B [hi, lo], as operands (a symmetric
+  // one also for its mirrored tiles) and as the epilogue's blocks
+  CUtensorMap x_gram[2][2], x_apply[2][2], x_block[2][2], ab_op[2][2], ab_block[2][2], ab_mirror[2];
+  for (int j = 0; j < 2; ++j) {
+    for (int i = 0; i < 2; ++i) {
+      const void* x = b + L.x[i][j];
+      MOE_TRY(make_ns_map(&x_gram[i][j], x, cols, rows, G, L.ld, wide ? 128 : 64, 64));
+      MOE_TRY(make_ns_map(&x_apply[i][j], x, cols, rows, G, L.ld, wide ? 64 : 128, 64));
+      MOE_TRY(make_ns_map(&x_block[i][j], x, cols, rows, G, L.ld, 32, 32));
+      const void* ab = b + (i == 0 ? L.a[j] : L.b[j]);
+      if (PAIR && j) {  // A and B have no lo part there: not read
+        ab_op[i][j] = ab_op[i][0];
+        ab_block[i][j] = ab_block[i][0];
+        continue;
+      }
+      MOE_TRY(make_ns_map(&ab_op[i][j], ab, r, r, G, L.ldr, 128, 64));
+      MOE_TRY(make_ns_map(&ab_block[i][j], ab, r, r, G, L.ldr, 32, 32));
+      if (j == 0) MOE_TRY(make_ns_map(&ab_mirror[i], ab, r, r, G, L.ldr, 64, 64));
+    }
+  }
   NsParams sym;
   memset(&sym, 0, sizeof(sym));
   sym.M = sym.N = r;
   sym.n_tiles = rt;
   sym.per_group = rt * (rt + 1) / 2;
   sym.total = c.groups * sym.per_group;
-  sym.ld = L.ldr;
-  sym.stride = static_cast<int64_t>(r) * L.ldr;
   sym.status = status_ptr(b);
   for (int k = 0; k < c.steps; ++k) {
     const int in = k & 1;
     // A = X X^T or X^T X
     NsParams g = sym;
-    const uint32_t box = wide ? 128 : 64;
-    MOE_TRY(make_ns_map(&g.a, b + L.x[in][0], cols, rows, G, L.ld, box));
-    MOE_TRY(make_ns_map(&g.a_lo, b + L.x[in][1], cols, rows, G, L.ld, box));
-    g.b = g.a;
-    g.b_lo = g.a_lo;
+    g.a = g.b = x_gram[in][0];
+    g.a_lo = g.b_lo = x_gram[in][1];
     g.ksteps = ((wide ? c.cols : c.rows) + kNsBK - 1) / kNsBK;
-    g.out_hi = half_at(L.a[0]);
-    g.out_lo = half_at(L.a[1]);
+    g.in_hi = g.in_lo = g.w_in = g.sym = ab_block[0][0];  // not read
+    g.out_hi = ab_block[0][0];
+    g.out_lo = ab_block[0][1];
     g.out_diag = float_at(L.da);
     g.alpha = kNsSa / (kNsSx * kNsSx);
-    if (wide) MOE_TRY((launch_ns<kNsGram, false, false, PAIR, false>(g, s)));
-    else MOE_TRY((launch_ns<kNsGram, true, true, PAIR, false>(g, s)));
+    if (wide) MOE_TRY((launch_ns<kNsGram, false, PAIR, false>(g, s)));
+    else MOE_TRY((launch_ns<kNsGram, true, PAIR, false>(g, s)));
     // B = b A + c A^2
     NsParams q = sym;
-    MOE_TRY(make_ns_map(&q.a, b + L.a[0], r, r, G, L.ldr, 128));
-    MOE_TRY(make_ns_map(&q.a_lo, b + L.a[1], r, r, G, L.ldr, 128));
-    q.b = q.a;
-    q.b_lo = q.a_lo;
+    q.a = q.b = ab_op[0][0];
+    q.a_lo = q.b_lo = ab_op[0][1];
     q.ksteps = (r + kNsBK - 1) / kNsBK;
-    q.in_hi = half_at(L.a[0]);
-    q.in_lo = half_at(L.a[1]);
+    q.in_hi = q.w_in = ab_block[0][0];
+    q.in_lo = ab_block[0][1];
     q.in_diag = float_at(L.da);
-    q.out_hi = half_at(L.b[0]);
-    q.out_lo = half_at(L.b[1]);
+    q.out_hi = ab_block[1][0];
+    q.out_lo = ab_block[1][1];
+    q.sym = ab_mirror[0];
     q.out_diag = float_at(L.db);
     q.alpha = c.c * kNsSb / (kNsSa * kNsSa);
     q.beta = c.b * kNsSb / kNsSa;
-    MOE_TRY((launch_ns<kNsPoly, false, false, PAIR, false>(q, s)));
+    q.diag_scale = q.alpha;
+    MOE_TRY((launch_ns<kNsPoly, false, PAIR, false>(q, s)));
     // X' = a X + B X or a X + X B
     NsParams x;
     memset(&x, 0, sizeof(x));
     x.M = c.rows;
     x.N = c.cols;
-      x.n_tiles = tiles(c.cols);
+    x.n_tiles = tiles(c.cols);
     x.per_group = tiles(c.rows) * x.n_tiles;
     x.total = c.groups * x.per_group;
     x.ksteps = q.ksteps;
-    x.ld = L.ld;
-    x.stride = static_cast<int64_t>(c.rows) * L.ld;
-    x.in_hi = half_at(L.x[in][0]);
-    x.in_lo = half_at(L.x[in][1]);
-    x.out_hi = half_at(L.x[in ^ 1][0]);
-    x.out_lo = half_at(L.x[in ^ 1][1]);
+    x.a = wide ? ab_op[1][0] : x_apply[in][0];
+    x.a_lo = wide ? ab_op[1][1] : x_apply[in][1];
+    x.b = wide ? x_apply[in][0] : ab_op[1][0];
+    x.b_lo = wide ? x_apply[in][1] : ab_op[1][1];
+    x.in_hi = x_block[in][0];
+    x.in_lo = x_block[in][1];
+    x.out_hi = x_block[in ^ 1][0];
+    x.out_lo = x_block[in ^ 1][1];
+    x.w_in = x.in_hi;
+    x.sym = ab_mirror[1];
     x.in_diag = float_at(L.db);
     x.alpha = 1.f / kNsSb;
     x.beta = c.a;
     x.diag_scale = 1.f / kNsSb;
-    x.tall = wide ? 0 : 1;
     x.status = status_ptr(b);
+    if (k + 1 < c.steps) {
+      if (wide) MOE_TRY((launch_ns<kNsApply, false, PAIR, false>(x, s)));
+      else MOE_TRY((launch_ns<kNsApply, true, PAIR, false>(x, s)));
+      continue;
+    }
+    x.alpha /= kNsSx;  // X itself
+    x.beta /= kNsSx;
+    x.diag_scale /= kNsSx;
     x.out = u.out;
     x.w = u.w;
     x.keep = u.keep;
     x.step = u.step;
-    const bool last = k + 1 == c.steps;
-    CUtensorMap bm[2], xm[2];
-    for (int j = 0; j < 2; ++j) {
-      MOE_TRY(make_ns_map(&bm[j], b + L.b[j], r, r, G, L.ldr, 128));
-      MOE_TRY(make_ns_map(&xm[j], b + L.x[in][j], cols, rows, G, L.ld, wide ? 64 : 128));
+    x.tma_out = c.cols % 8 == 0 && aligned16(u.out) && aligned16(u.w) ? 1 : 0;
+    if (x.tma_out) {
+      MOE_TRY(make_ns_map(&x.out_hi, u.out, cols, rows, G, cols, 32, 32));
+      if (u.w) MOE_TRY(make_ns_map(&x.w_in, u.w, cols, rows, G, cols, 32, 32));
     }
-    x.a = wide ? bm[0] : xm[0];
-    x.a_lo = wide ? bm[1] : xm[1];
-    x.b = wide ? xm[0] : bm[0];
-    x.b_lo = wide ? xm[1] : bm[1];
-    if (wide) {
-      if (last) MOE_TRY((launch_ns<kNsApply, false, true, PAIR, true>(x, s)));
-      else MOE_TRY((launch_ns<kNsApply, false, true, PAIR, false>(x, s)));
-    } else {
-      if (last) MOE_TRY((launch_ns<kNsApply, false, false, PAIR, true>(x, s)));
-      else MOE_TRY((launch_ns<kNsApply, false, false, PAIR, false>(x, s)));
-    }
+    if (wide) MOE_TRY((launch_ns<kNsApply, false, PAIR, true>(x, s)));
+    else MOE_TRY((launch_ns<kNsApply, true, PAIR, true>(x, s)));
   }
   return MOE_OK;
 }
