@@ -200,8 +200,11 @@ def _cuda(t, dtype, name):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The stream's handle; by default the current stream of the current device (read as the
+    handle itself: the Stream object of torch.cuda.current_stream() takes 3 us to make)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(fn, code):
@@ -457,38 +460,54 @@ def moe_backward(cfg, weights, bwd_weights, saved: dict, dy, dx, workspace, dlog
     off, n_seq = _sequences(seq_offsets)
     _check("moe_backward_scored", lib().moe_backward_scored(
         ctypes.byref(cfg), ctypes.byref(router), *first,
-        _sized(dscore, f32, (n_seq, cfg.E), "dscore"), off, n_seq, _p(_cuda(dloss, f32, "dloss")),
+        _sized(dscore, f32, (n_seq, cfg.E), "dscore"), off, n_seq, _sized(dloss, f32, (1,), "dloss"),
         *last))
 
 
 def _sized(t, dtype, shape, name):
-    """_cuda with the shape checked too (the C call sees only the pointer)."""
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    return _p(_cuda(t, dtype, name))
+    """The address of a tensor of this type and shape, contiguous on the current device (the C
+    call sees only the address); None for None."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        dev = t.get_device()  # -1: host memory
+        if dev >= 0 and dev == torch._C._cuda_getDevice():
+            return t.data_ptr()
+    where = "" if not t.is_cuda else f", current device cuda:{torch.cuda.current_device()}"
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on the "
+                     f"current CUDA device, got {t.dtype} of shape {tuple(t.shape)} on {t.device} "
+                     f"(contiguous={t.is_contiguous()}{where})")
+
+
+def _scratch(workspace):
+    """Address and bytes of a workspace."""
+    if workspace is None:
+        return None, 0
+    return workspace.data_ptr(), workspace.numel()
 
 
 def moe_route_scored(cfg, router, topk_idx, topk_w, x=None, w_router=None, bias=None,
                      workspace=None, logits_in=None, logits_out=None, stream=None):
     """Routing by softmax or sigmoid scores: from x and w_router (with a workspace and
     logits_out), or from the logits alone (logits_in)."""
-    bf, f32, T, E = torch.bfloat16, torch.float32, cfg.T, cfg.E
-    k = cfg.top_k
+    bf, f32, T, E, k = torch.bfloat16, torch.float32, cfg.T, cfg.E, cfg.top_k
     _check("moe_route_scored", lib().moe_route_scored(
-        ctypes.byref(cfg), ctypes.byref(router), _sized(x, bf, (T, cfg.H), "x"),
+        cfg, router, _sized(x, bf, (T, cfg.H), "x"),
         _sized(w_router, bf, (E, cfg.H), "w_router"), _sized(bias, f32, (E,), "bias"),
         _sized(logits_in, f32, (T, E), "logits_in"),
         _sized(logits_out, f32, (T, E), "logits_out"),
         _sized(topk_idx, torch.int32, (T, k), "topk_idx"), _sized(topk_w, f32, (T, k), "topk_w"),
-        _p(workspace), workspace.numel() if workspace is not None else 0, _stream(stream)))
+        *_scratch(workspace), _stream(stream)))
 
 
-def _sequences(seq_offsets, name="seq_offsets"):
+def _sequences(seq_offsets):
+    """Address and number of the sequences that the offsets bound (None: one of all rows)."""
     if seq_offsets is None:
         return None, 1
     if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
-        raise ValueError(f"{name}: expected at least two offsets in one dimension")
-    return _p(_cuda(seq_offsets, torch.int32, name)), seq_offsets.numel() - 1
+        raise ValueError("seq_offsets: expected at least two offsets in one dimension")
+    n = seq_offsets.numel()
+    return _sized(seq_offsets, torch.int32, (n,), "seq_offsets"), n - 1
 
 
 def moe_route_backward(cfg, router, logits, topk_idx, dgate, dlogits, dscore=None,
@@ -498,9 +517,9 @@ def moe_route_backward(cfg, router, logits, topk_idx, dgate, dlogits, dscore=Non
     f32, T, E, k = torch.float32, cfg.T, cfg.E, cfg.top_k
     off, n_seq = _sequences(seq_offsets)
     _check("moe_route_backward", lib().moe_route_backward(
-        ctypes.byref(cfg), ctypes.byref(router), _sized(logits, f32, (T, E), "logits"),
+        cfg, router, _sized(logits, f32, (T, E), "logits"),
         _sized(topk_idx, torch.int32, (T, k), "topk_idx"), _sized(dgate, f32, (T, k), "dgate"),
-        _sized(dscore, f32, (n_seq, E), "dscore"), off, n_seq, _p(_cuda(dloss, f32, "dloss")),
+        _sized(dscore, f32, (n_seq, E), "dscore"), off, n_seq, _sized(dloss, f32, (1,), "dloss"),
         _sized(dlogits, f32, (T, E), "dlogits"), _stream(stream)))
 
 
@@ -517,11 +536,10 @@ def moe_balance_loss(cfg, router, logits, topk_idx, coef, loss, load, dscore, wo
     f32, i32, T, E = torch.float32, torch.int32, cfg.T, cfg.E
     off, n_seq = _sequences(seq_offsets)
     _check("moe_balance_loss", lib().moe_balance_loss(
-        ctypes.byref(cfg), ctypes.byref(router), _sized(logits, f32, (T, E), "logits"),
+        cfg, router, _sized(logits, f32, (T, E), "logits"),
         _sized(topk_idx, i32, (T, cfg.top_k), "topk_idx"), off, n_seq, coef,
         _sized(loss, f32, (1,), "loss"), _sized(load, i32, (n_seq, E), "load"),
-        _sized(dscore, f32, (n_seq, E), "dscore"), _p(workspace), workspace.numel(),
-        _stream(stream)))
+        _sized(dscore, f32, (n_seq, E), "dscore"), *_scratch(workspace), _stream(stream)))
 
 
 GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -534,39 +552,35 @@ def moe_muon_workspace_size(mcfg) -> int:
     return n.value
 
 
+def _stacked(mcfg, t, dtype, name):
+    """A contiguous stack of the config's matrices (a single matrix may be 2-D)."""
+    shape = (mcfg.groups, mcfg.rows, mcfg.cols)
+    return _sized(t, dtype, shape[1:] if mcfg.groups == 1 and t.dim() == 2 else shape, name)
+
+
 def _grad(mcfg, t, name):
     if t.dtype not in GRAD_DTYPES:
         raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
     return _stacked(mcfg, t, t.dtype, name), GRAD_DTYPES[t.dtype]
 
 
-def _stacked(mcfg, t, dtype, name):
-    """A contiguous stack of the config's matrices (a single matrix may be 2-D)."""
-    shape = (mcfg.groups, mcfg.rows, mcfg.cols)
-    if tuple(t.shape) != shape and not (mcfg.groups == 1 and tuple(t.shape) == shape[1:]):
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    return _p(_cuda(t, dtype, name))
-
-
 def moe_orthogonalize(mcfg, g, out, workspace, stream=None):
     """out (bf16) = each matrix of g (fp32 or bf16) with its singular values moved to about 1."""
-    gp, gd = _grad(mcfg, g, "g")
     _check("moe_orthogonalize", lib().moe_orthogonalize(
-        ctypes.byref(mcfg), gp, gd, _stacked(mcfg, out, torch.bfloat16, "out"), _p(workspace),
-        workspace.numel(), _stream(stream)))
+        mcfg, *_grad(mcfg, g, "g"), _stacked(mcfg, out, torch.bfloat16, "out"),
+        *_scratch(workspace), _stream(stream)))
 
 
 def moe_muon_step(mcfg, grad, momentum, momentum_out, w, w_out, workspace, beta=0.95,
                   nesterov=True, step=0.02, decay=0.0, stream=None):
     """Momentum, orthogonalised update and weights of one optimiser step; ``momentum_out`` may
     be ``momentum`` and ``w_out`` may be ``w``."""
-    gp, gd = _grad(mcfg, grad, "grad")
     f32, bf = torch.float32, torch.bfloat16
     _check("moe_muon_step", lib().moe_muon_step(
-        ctypes.byref(mcfg), gp, gd, _stacked(mcfg, momentum, f32, "momentum"),
+        mcfg, *_grad(mcfg, grad, "grad"), _stacked(mcfg, momentum, f32, "momentum"),
         _stacked(mcfg, momentum_out, f32, "momentum_out"), beta, 1 if nesterov else 0,
         _stacked(mcfg, w, bf, "w"), _stacked(mcfg, w_out, bf, "w_out"), step, decay,
-        _p(workspace), workspace.numel(), _stream(stream)))
+        *_scratch(workspace), _stream(stream)))
 
 
 class MoELayer:

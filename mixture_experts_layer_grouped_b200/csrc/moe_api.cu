@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -14,6 +15,7 @@
 #include "backward.cuh"
 #include "grouped_gemm.cuh"
 #include "muon.cuh"
+#include "muon_small.cuh"
 #include "prepare.cuh"
 #include "quantize.cuh"
 #include "route_permute_combine.cuh"

@@ -1,6 +1,6 @@
 // Host side of the orthogonalised updates (part of moe_api.cu's translation unit): the
 // workspace layout, the launches and the C ABI calls of include/moe_b200.h's Muon section.
-// The kernels are in muon.cuh.
+// The kernels are in muon.cuh and muon_small.cuh.
 #pragma once
 
 namespace {
@@ -10,8 +10,81 @@ struct MuonLayout {
   int r, ld, ldr, chunk, chunks;
 };
 
+// What the steps can reach from singular values in [0, 1], interval by interval: with
+// x = sigma^2 in [0, R^2], the extremes of f(sigma) = sigma (a + b x + c x^2), of a + b x + c x^2
+// and of b x + c x^2 lie at the interval's end or where their derivatives vanish.
+struct MuonBounds {
+  bool ok;      // inside what the fp16 scales hold: |f| < 1.9, |b x + c x^2| < 7.9
+  double p, q;  // the largest |a + b x + c x^2|, and the product of the steps'
+};
+
+MuonBounds muon_bounds(const moe_muon_config& cfg) {
+  const double a = cfg.a, b = cfg.b, c = cfg.c;
+  MuonBounds r{true, 0.0, 1.0};
+  double X = 1.0;  // R^2
+  for (int s = 0; s < cfg.steps; ++s) {
+    double at[6] = {0.0, X, 0.0, 0.0, 0.0, 0.0};
+    int n = 2;
+    auto add = [&](double x) { if (x > 0.0 && x < X) at[n++] = x; };
+    if (c != 0.0) {
+      add(-b / (2.0 * c));  // of the polynomial itself
+      const double d = 9.0 * b * b - 20.0 * a * c;
+      if (d >= 0.0) {
+        add((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+        add((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+      }
+    } else if (b != 0.0) {
+      add(-a / (3.0 * b));
+    }
+    double next = 0.0, most = 0.0;
+    for (int i = 0; i < n; ++i) {
+      const double x = at[i], poly = b * x + c * x * x, f = (a + poly) * std::sqrt(x);
+      if (!(std::fabs(poly) < 7.9) || !(std::fabs(f) < 1.9)) r.ok = false;
+      next = std::fmax(next, std::fabs(f));
+      most = std::fmax(most, std::fabs(a + poly));
+    }
+    if (!r.ok) break;
+    r.p = std::fmax(r.p, most);
+    r.q *= most;
+    X = next * next;
+  }
+  return r;
+}
+
 // One-CTA tiles and products of hi and lo parts for matrices of at most 128 rows or columns.
 bool muon_split(const moe_muon_config& c) { return c.rows <= 128 || c.cols <= 128; }
+
+// The r x r form (muon_small.cuh) where one extent is at most 128 and Q stays small: its
+// 22 bits are then 2^-22 * 1024 of the result or better.
+bool muon_small(const moe_muon_config& c) {
+  if (!muon_split(c)) return false;
+  const MuonBounds m = muon_bounds(c);
+  return m.q <= 1024.0 && m.p <= 15.0;
+}
+
+struct MuonSmallLayout {
+  size_t status, part, part_exp, q, inv_norm, total;
+  int pieces, parts;
+};
+
+MuonSmallLayout muon_small_layout(const moe_muon_config& c) {
+  MuonSmallLayout L;
+  const size_t G = c.groups;
+  const int n = c.rows > c.cols ? c.rows : c.cols;
+  L.pieces = (n + 127) / 128;
+  // parts of a matrix's sum: enough CTAs for two rounds of the GPU, but one CTA adds them up
+  int parts = (2 * 148 + c.groups - 1) / c.groups;
+  if (parts > kMsMaxParts) parts = kMsMaxParts;
+  L.parts = parts < L.pieces ? parts : L.pieces;
+  size_t o = 0;
+  L.status = o; o = align_up(o + 4);
+  L.part = o; o = align_up(o + G * L.parts * 16 * kMsThreads * 16);
+  L.part_exp = o; o = align_up(o + G * L.parts * 4);
+  L.q = o; o = align_up(o + G * 2 * kMsImage);
+  L.inv_norm = o; o = align_up(o + G * 8);
+  L.total = o;
+  return L;
+}
 
 MuonLayout muon_layout(const moe_muon_config& c) {
   MuonLayout L;
@@ -43,26 +116,6 @@ MuonLayout muon_layout(const moe_muon_config& c) {
   return L;
 }
 
-// The largest |singular value| that the steps can reach from [0, 1], and the largest
-// |b x + c x^2| on the way, must stay inside what the fp16 scales hold.
-bool muon_bounded(const moe_muon_config& c) {
-  const int kPoints = 4096;
-  double R = 1.0;
-  for (int s = 0; s < c.steps; ++s) {
-    double next = 0.0;
-    for (int i = 0; i <= kPoints; ++i) {
-      const double v = R * i / kPoints, x = v * v;
-      const double poly = static_cast<double>(c.b) * x + static_cast<double>(c.c) * x * x;
-      const double y = (c.a + poly) * v;
-      if (!(poly > -7.9 && poly < 7.9)) return false;
-      if (!(y > -1.9 && y < 1.9)) return false;
-      next = y < 0 ? (-y > next ? -y : next) : (y > next ? y : next);
-    }
-    R = next;
-  }
-  return true;
-}
-
 moe_status check_muon(const moe_muon_config* c) {
   if (!c) return MOE_ERR_INVALID_ARG;
   if (c->groups < 1 || c->rows < 1 || c->cols < 1 || c->steps < 1 || c->steps > 64)
@@ -71,7 +124,7 @@ moe_status check_muon(const moe_muon_config* c) {
   if (c->groups > 65535) return MOE_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(c->rows) * ((static_cast<int64_t>(c->cols) + 7) / 8 * 8) > (int64_t(1) << 30))
     return MOE_ERR_UNSUPPORTED;
-  if (!muon_bounded(*c)) return MOE_ERR_UNSUPPORTED;
+  if (!muon_bounds(*c).ok) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -256,7 +309,69 @@ moe_status ns_steps(const moe_muon_config& c, const MuonArgs& u, const MuonLayou
   return MOE_OK;
 }
 
+template <typename K>
+moe_status launch_ms(K kern, dim3 grid, int smem, cudaStream_t s, const MuonSmallArgs& a) {
+  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  MOE_TRY(launch_pdl(kern, grid, dim3(kMsThreads), smem, s, a));
+  return launch_check();
+}
+
+moe_status muon_small_run(const moe_muon_config& c, const MuonArgs& u, void* ws, cudaStream_t s) {
+  const MuonSmallLayout L = muon_small_layout(c);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  MuonSmallArgs a;
+  memset(&a, 0, sizeof(a));
+  a.grad = u.grad;
+  a.mom_in = u.mom_in;
+  a.mom_out = u.mom_out;
+  a.w = u.w;
+  a.out = u.out;
+  a.part = reinterpret_cast<float4*>(b + L.part);
+  a.part_exp = reinterpret_cast<int32_t*>(b + L.part_exp);
+  a.q = b + L.q;
+  a.inv_norm = reinterpret_cast<double*>(b + L.inv_norm);
+  a.rows = c.rows;
+  a.cols = c.cols;
+  a.tall = c.rows > c.cols ? 1 : 0;
+  a.r = a.tall ? c.cols : c.rows;
+  a.r16 = (a.r + 15) / 16 * 16;
+  a.pieces = L.pieces;
+  a.parts = L.parts;
+  a.steps = c.steps;
+  a.nesterov = u.nesterov ? 1 : 0;
+  a.beta = u.beta;
+  a.a = c.a;
+  a.b = c.b;
+  a.c = c.c;
+  a.eps = c.eps;
+  a.keep = u.keep;
+  a.step = u.step;
+  a.sq = std::exp2(std::floor(std::log2(60000.0 / std::fmax(muon_bounds(c).q, 1.0))));
+  a.status = status_ptr(b);
+  const bool vec = c.cols % 4 == 0 && aligned16(u.grad) && aligned16(u.mom_in) && aligned16(u.mom_out);
+  const bool out_vec = c.cols % 4 == 0 && aligned16(u.out) && aligned16(u.w);
+  const dim3 grid(static_cast<unsigned>(L.parts), static_cast<unsigned>(c.groups));
+  int applies = (sm_count() + c.groups - 1) / c.groups;  // CTAs a matrix: one round of the GPU
+  if (applies > L.pieces) applies = L.pieces;
+  const dim3 agrid(static_cast<unsigned>(applies), static_cast<unsigned>(c.groups));
+  auto run = [&](auto gram, auto apply) -> moe_status {
+    MOE_TRY(launch_ms(gram, grid, kMsGramSmem, s, a));
+    MOE_TRY(launch_ms(muon_chain_kernel, dim3(c.groups), kMsChainSmem, s, a));
+    return launch_ms(apply, agrid, kMsApplySmem, s, a);
+  };
+  using bf = __nv_bfloat16;
+  if (u.grad_bf16) {
+    if (vec) return out_vec ? run(muon_gram_kernel<bf, true>, muon_apply_kernel<bf, true, true>)
+                            : run(muon_gram_kernel<bf, true>, muon_apply_kernel<bf, true, false>);
+    return run(muon_gram_kernel<bf, false>, muon_apply_kernel<bf, false, false>);
+  }
+  if (vec) return out_vec ? run(muon_gram_kernel<float, true>, muon_apply_kernel<float, true, true>)
+                          : run(muon_gram_kernel<float, true>, muon_apply_kernel<float, true, false>);
+  return run(muon_gram_kernel<float, false>, muon_apply_kernel<float, false, false>);
+}
+
 moe_status muon_run(const moe_muon_config& c, const MuonArgs& u, void* ws, cudaStream_t s) {
+  if (muon_small(c)) return muon_small_run(c, u, ws, s);
   const MuonLayout L = muon_layout(c);
   uint8_t* b = static_cast<uint8_t*>(ws);
   MuonInArgs a;
@@ -293,12 +408,16 @@ moe_status muon_run(const moe_muon_config& c, const MuonArgs& u, void* ws, cudaS
   return muon_split(c) ? ns_steps<false>(c, u, L, b, s) : ns_steps<true>(c, u, L, b, s);
 }
 
+size_t muon_bytes(const moe_muon_config& c) {
+  return muon_small(c) ? muon_small_layout(c).total : muon_layout(c).total;
+}
+
 moe_status check_muon_call(const moe_muon_config* cfg, const void* grad, int32_t grad_dtype,
                            void* ws, size_t bytes) {
   MOE_TRY(check_muon(cfg));
   if (!grad || (grad_dtype != MOE_GRAD_FP32 && grad_dtype != MOE_GRAD_BF16)) return MOE_ERR_INVALID_ARG;
   if (!ws || reinterpret_cast<uintptr_t>(ws) % kAlign) return MOE_ERR_INVALID_ARG;
-  if (bytes < muon_layout(*cfg).total) return MOE_ERR_WORKSPACE;
+  if (bytes < muon_bytes(*cfg)) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
@@ -309,7 +428,7 @@ extern "C" {
 moe_status moe_muon_workspace_size(const moe_muon_config* cfg, size_t* bytes) {
   MOE_TRY(check_muon(cfg));
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = muon_layout(*cfg).total;
+  *bytes = muon_bytes(*cfg);
   return MOE_OK;
 }
 

@@ -1,0 +1,527 @@
+// Orthogonalised updates of matrices with at most 128 rows or 128 columns (r of them; n is
+// the other extent), in three kernels.  X_5 = Q X_0 where Q is a polynomial of S = X_0 X_0^T,
+// and with S_k = X_k X_k^T the steps never touch X:
+//
+//   P = a I + b S + c S^2,   Q <- P Q,   S <- P S P       (all r x r, all commuting),
+//
+//   muon_gram_kernel    momentum; partial sums of u u^T over 128-wide pieces of n;
+//   muon_chain_kernel   one CTA a matrix: S = sum / (|u|_F + eps)^2 (the trace is |u|_F^2),
+//                       then every step in shared memory and TMEM;
+//   muon_apply_kernel   X = Q u / (|u|_F + eps) and the weights, 128-wide pieces of n.
+//
+// So u is read twice whatever the number of steps, and nothing of it is stored between.
+// Every product takes fp16 hi and lo parts (hi hi + hi lo + lo hi, 22 bits): the square roots
+// of S's roundings are what small singular values see, and with 11 bits those would be gone.
+// Measured against 64 bits: 1e-6 (full rank) to 1e-3 (rank 1), far below the bf16 result.
+// The pieces are scaled by a power of two from their largest value; partial sums carry the
+// exponent, so the range of fp32 gradients is covered.
+#pragma once
+
+#include "muon.cuh"
+
+namespace moe {
+
+constexpr int kMsThreads = 256;
+constexpr int kMsBlock = 128 * 128;          // bytes of 128 rows x 64 fp16
+constexpr int kMsImage = 2 * kMsBlock;       // 128 x 128 fp16: two such blocks
+constexpr int kMsMaxParts = 16;
+constexpr float kMsSs = 16384.f, kMsSp = 4096.f, kMsSt = 8192.f;  // scales of S, P, P S
+
+struct MuonSmallArgs {
+  const void* grad;         // [groups, rows, cols] fp32 or bf16
+  const float* mom_in;      // or null: no momentum
+  float* mom_out;
+  const __nv_bfloat16* w;   // or null: out = X
+  __nv_bfloat16* out;
+  float4* part;             // [groups, parts, 16, 256]: the threads' 64 sums each
+  int32_t* part_exp;        // [groups, parts]: the sums are u u^T 2^(2 exp)
+  uint8_t* q;               // [groups, 2, kMsImage]: Q's shared-memory images, hi and lo
+  double* inv_norm;         // [groups]: 1 / (|u|_F + eps), over Q's scale
+  int rows, cols, r, r16, pieces, parts, steps;  // r16: r rounded up to 16
+  int tall, nesterov;
+  float beta, a, b, c, eps, keep, step, sq;      // sq: scale of Q
+  int32_t* status;
+};
+
+// Byte offset of element (row, col) in an image: blocks of 64 columns, 128-byte swizzle.
+__device__ __forceinline__ int ms_at(int row, int col) {
+  return (col >> 6) * kMsBlock + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4) + (col & 7) * 2;
+}
+
+__device__ __forceinline__ float pow2f(int e) {  // 2^e, e in [-126, 127]
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Four neighbouring fp32 values as hi and lo parts of an image pair.
+__device__ __forceinline__ void ms_store4(uint8_t* hi, uint8_t* lo, int row, int col, float4 v) {
+  const __half2 h0 = __floats2half2_rn(v.x, v.y), h1 = __floats2half2_rn(v.z, v.w);
+  const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+  const __half2 l0 = __floats2half2_rn(v.x - f0.x, v.y - f0.y), l1 = __floats2half2_rn(v.z - f1.x, v.w - f1.y);
+  const int at = ms_at(row, col);
+  *reinterpret_cast<uint2*>(hi + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&h0),
+                                                  *reinterpret_cast<const uint32_t*>(&h1));
+  *reinterpret_cast<uint2*>(lo + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&l0),
+                                                  *reinterpret_cast<const uint32_t*>(&l1));
+}
+
+// D (+)= A B^T over K of two image pairs, hi hi + hi lo + lo hi (one thread issues).
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ void ms_mma(uint32_t d, uint32_t a_hi, uint32_t a_lo, uint32_t b_hi,
+                                       uint32_t b_lo, int N, int K) {
+  const uint32_t idesc = idesc_f16(128, N, A_MN, B_MN);
+  uint32_t accum = 0u;
+  for (int pass = 0; pass < 3; ++pass) {
+    const uint32_t a = pass == 2 ? a_lo : a_hi, b = pass == 1 ? b_lo : b_hi;
+    for (int k = 0; k < K; k += 16) {
+      // K-major: 16 of K inside a block, 64 to the next block; MN-major: rows of 128 bytes
+      const uint64_t da = A_MN ? sdesc_mnmajor_sw128(a + k * 128, kMsBlock)
+                               : sdesc_kmajor_sw128(a + (k >> 6) * kMsBlock) + ((k & 63) >> 3);
+      const uint64_t db = B_MN ? sdesc_mnmajor_sw128(b + k * 128, kMsBlock)
+                               : sdesc_kmajor_sw128(b + (k >> 6) * kMsBlock) + ((k & 63) >> 3);
+      mma_bf16(d, da, db, idesc, accum);
+      accum = 1u;
+    }
+  }
+}
+
+// u of a 128 x 128 piece, 16 rows a warp and four columns a lane; FIRST: the momentum is
+// formed and written, otherwise it is read back.
+template <typename T, bool VEC, bool FIRST>
+__device__ __forceinline__ void ms_load(const MuonSmallArgs& a, int g, int piece, float4 (&u)[16]) {
+  const int warp = warp_id(), lane = lane_id();
+  const int r0 = a.tall ? piece * 128 : 0, c0 = a.tall ? 0 : piece * 128;
+  const int64_t base = static_cast<int64_t>(g) * a.rows * a.cols;
+  const T* grad = static_cast<const T*>(a.grad) + base;
+  const float* mom = (FIRST ? a.mom_in : a.mom_out);
+  const bool need_g = FIRST || !mom || a.nesterov;
+  const int col = c0 + 4 * lane;
+  const int r_end = min(a.rows, r0 + 128);
+  float4 m[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int row = r0 + warp + 8 * i;
+    u[i] = m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row >= r_end || col >= a.cols) continue;
+    const int64_t at = static_cast<int64_t>(row) * a.cols + col;
+    if constexpr (VEC) {
+      if (need_g) u[i] = load4<T>(grad + at);
+      if (mom) m[i] = *reinterpret_cast<const float4*>(mom + base + at);
+    } else {
+      float* up = &u[i].x;
+      float* mp = &m[i].x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (col + j < a.cols) {
+          if (need_g) up[j] = load1(grad + at + j);
+          if (mom) mp[j] = mom[base + at + j];
+        }
+    }
+  }
+  if (!mom) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int row = r0 + warp + 8 * i;
+    float* up = &u[i].x;
+    float* mp = &m[i].x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (FIRST) mp[j] = fmaf(a.beta, mp[j], up[j]);
+      up[j] = a.nesterov ? fmaf(a.beta, mp[j], up[j]) : mp[j];
+    }
+    if (FIRST && row < r_end && col < a.cols) {
+      const int64_t at = base + static_cast<int64_t>(row) * a.cols + col;
+      if constexpr (VEC) {
+        *reinterpret_cast<float4*>(a.mom_out + at) = m[i];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col + j < a.cols) a.mom_out[at + j] = mp[j];
+      }
+    }
+  }
+}
+
+// The piece's image pair, scaled so that its largest value is in [2^13, 2^14); returns the
+// exponent of the scale.  Rows past what the products read are left out.
+__device__ __forceinline__ int ms_image(const MuonSmallArgs& a, float4 (&u)[16], uint8_t* hi, uint8_t* lo,
+                                        float* red) {
+  const int warp = warp_id(), lane = lane_id();
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    m = fmaxf(fmaxf(fmaxf(m, fabsf(u[i].x)), fmaxf(fabsf(u[i].y), fabsf(u[i].z))), fabsf(u[i].w));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+  m = red[0];
+#pragma unroll
+  for (int i = 1; i < kMsThreads / 32; ++i) m = fmaxf(m, red[i]);
+  // exponent of the largest value (an infinity or zero: no scale; far below fp32: clamped)
+  const int em = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+  const int e = (m == 0.f || em == 128) ? 0 : min(13 - em, 126);
+  const float s = pow2f(max(e, -126));
+  const int rows = a.tall ? 128 : a.r16;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int row = warp + 8 * i;
+    if (row >= rows) break;
+    ms_store4(hi, lo, row, 4 * lane, make_float4(u[i].x * s, u[i].y * s, u[i].z * s, u[i].w * s));
+  }
+  return max(e, -126);
+}
+
+// Shared parts of the three kernels: TMEM, one mbarrier for the products, flags.
+struct MsCtl {
+  uint64_t bar;
+  uint32_t tmem;
+  int abort;
+  float red[kMsThreads / 32];
+};
+
+__device__ __forceinline__ uint32_t ms_begin(MsCtl* ctl, uint32_t cols) {
+  if (threadIdx.x == 0) {
+    mbar_init(&ctl->bar, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp_id() == 0) {
+    tmem_alloc(&ctl->tmem, cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  return ctl->tmem;
+}
+__device__ __forceinline__ void ms_end(uint32_t tmem, uint32_t cols) {
+  tc_fence_before();
+  __syncthreads();
+  if (warp_id() == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, cols);
+  }
+}
+// The products issued since the last call are done, for the whole block (false: gave up).
+__device__ __forceinline__ bool ms_wait(MsCtl* ctl, uint32_t& phase, int32_t* status) {
+  const bool ok = mbar_wait(&ctl->bar, phase, &ctl->abort, status);
+  phase ^= 1;
+  const bool all = __syncthreads_and(ok);
+  tc_fence_after();
+  return all;
+}
+// Shared memory written by the block is what the tensor cores read next.
+__device__ __forceinline__ void ms_publish() {
+  fence_proxy_async_shared();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+
+constexpr int kMsCtlBytes = 256;
+constexpr int kMsGramSmem = 1024 + 2 * kMsImage + kMsCtlBytes;
+constexpr int kMsChainSmem = 1024 + 6 * kMsImage + kMsCtlBytes;
+constexpr int kMsApplySmem = 1024 + 4 * kMsImage + kMsCtlBytes;
+
+__device__ __forceinline__ uint8_t* ms_smem(uint8_t* raw) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+}
+
+// Grid (parts, groups): part p of a matrix takes pieces p, p + parts, ...
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kMsThreads) muon_gram_kernel(const __grid_constant__ MuonSmallArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* hi = ms_smem(smem_raw);
+  uint8_t* lo = hi + kMsImage;
+  MsCtl* ctl = reinterpret_cast<MsCtl*>(lo + kMsImage);
+  const uint32_t tmem = ms_begin(ctl, 128);
+  pdl_wait();
+  pdl_trigger();
+  const int warp = warp_id(), lane = lane_id(), g = blockIdx.y;
+  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 64;
+  float acc[64];
+#pragma unroll
+  for (int j = 0; j < 64; ++j) acc[j] = 0.f;
+  int exp = 0;
+  bool first = true, ok = true;
+  uint32_t phase = 0;
+  for (int piece = blockIdx.x; piece < a.pieces && ok; piece += a.parts) {
+    float4 u[16];
+    ms_load<T, VEC, true>(a, g, piece, u);
+    const int e = ms_image(a, u, hi, lo, ctl->red);
+    ms_publish();
+    if (threadIdx.x == 0) {
+      const uint32_t h = smem_u32(hi), l = smem_u32(lo);
+      if (a.tall) ms_mma<true, true>(tmem, h, l, h, l, a.r16, 128);
+      else ms_mma<false, false>(tmem, h, l, h, l, a.r16, 128);
+      mma_commit(&ctl->bar);
+    }
+    ok = ms_wait(ctl, phase, a.status);
+    if (!ok) break;
+    // the sums keep the smaller exponent: what has the larger one is scaled down
+    float f_acc = 1.f, f_new = 1.f;
+    if (first) {
+      exp = e;
+    } else if (e < exp) {
+      f_acc = 2 * (e - exp) < -126 ? 0.f : pow2f(2 * (e - exp));
+      exp = e;
+    } else {
+      f_new = 2 * (exp - e) < -126 ? 0.f : pow2f(2 * (exp - e));
+    }
+    first = false;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(taddr + 32 * h, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        acc[32 * h + j] = fmaf(__uint_as_float(v[j]), f_new, acc[32 * h + j] * f_acc);
+    }
+    tc_fence_before();
+    __syncthreads();  // images and TMEM may be written again
+    tc_fence_after();
+  }
+  const int64_t slot = static_cast<int64_t>(g) * a.parts + blockIdx.x;
+  if (row < a.r16) {
+    float4* dst = a.part + slot * 16 * kMsThreads + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (c0 + 4 * i < a.r16) dst[i * kMsThreads] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+  }
+  if (threadIdx.x == 0) a.part_exp[slot] = exp;
+  ms_end(tmem, 128);
+}
+
+// One CTA a matrix.  A thread holds half a row of S in fp32; P, Q and S (or P S) live in
+// shared memory as image pairs.  Three dependent products a step, about 1 us each.
+__global__ void __launch_bounds__(kMsThreads) muon_chain_kernel(const __grid_constant__ MuonSmallArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = ms_smem(smem_raw);
+  uint8_t *s_hi = base, *s_lo = base + kMsImage, *p_hi = base + 2 * kMsImage, *p_lo = base + 3 * kMsImage,
+          *q_hi = base + 4 * kMsImage, *q_lo = base + 5 * kMsImage;
+  MsCtl* ctl = reinterpret_cast<MsCtl*>(base + 6 * kMsImage);
+  const uint32_t tmem = ms_begin(ctl, 256);
+  pdl_wait();
+  pdl_trigger();
+  const int warp = warp_id(), lane = lane_id(), g = blockIdx.x;
+  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 64;
+  const bool mine = row < a.r16 && c0 < a.r16;
+  const int vecs = mine ? min(16, (a.r16 - c0) / 4) : 0;  // of four columns
+  // S: the parts under one exponent
+  int exp = 126;
+  for (int p = 0; p < a.parts; ++p) exp = min(exp, __ldg(a.part_exp + g * a.parts + p));
+  float4 s[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = 0; p < a.parts; ++p) {
+    const int64_t slot = static_cast<int64_t>(g) * a.parts + p;
+    const int d = 2 * (exp - __ldg(a.part_exp + slot));
+    const float f = d < -126 ? 0.f : pow2f(d);
+    const float4* src = a.part + slot * 16 * kMsThreads + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < vecs) {
+        const float4 v = __ldg(src + i * kMsThreads);
+        s[i].x = fmaf(v.x, f, s[i].x);
+        s[i].y = fmaf(v.y, f, s[i].y);
+        s[i].z = fmaf(v.z, f, s[i].z);
+        s[i].w = fmaf(v.w, f, s[i].w);
+      }
+  }
+  // |u|^2 2^(2 exp) is the trace
+  float diag = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (row == c0 + 4 * i) diag = s[i].x;
+    if (row == c0 + 4 * i + 1) diag = s[i].y;
+    if (row == c0 + 4 * i + 2) diag = s[i].z;
+    if (row == c0 + 4 * i + 3) diag = s[i].w;
+  }
+  if (!mine) diag = 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) diag += __shfl_xor_sync(0xffffffffu, diag, o);
+  if (lane == 0) ctl->red[warp] = diag;
+  __syncthreads();
+  double trace = 0.0;
+  for (int i = 0; i < kMsThreads / 32; ++i) trace += ctl->red[i];
+  const double up = ldexp(1.0, -exp);
+  const double inv = 1.0 / (sqrt(trace) * up + a.eps);
+  if (threadIdx.x == 0) a.inv_norm[g] = inv / a.sq;
+  const float f0 = static_cast<float>(up * inv);  // (its square may be past fp32)
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    s[i].x = s[i].x * f0 * f0;
+    s[i].y = s[i].y * f0 * f0;
+    s[i].z = s[i].z * f0 * f0;
+    s[i].w = s[i].w * f0 * f0;
+  }
+  auto put = [&](uint8_t* hi, uint8_t* lo, int i, float4 v, float f) {
+    if (i < vecs) ms_store4(hi, lo, row, c0 + 4 * i, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+  };
+#pragma unroll
+  for (int i = 0; i < 16; ++i) put(s_hi, s_lo, i, s[i], kMsSs);
+  const uint32_t S[2] = {smem_u32(s_hi), smem_u32(s_lo)}, P[2] = {smem_u32(p_hi), smem_u32(p_lo)},
+                 Q[2] = {smem_u32(q_hi), smem_u32(q_lo)};
+  const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
+  uint32_t phase = 0;
+  bool ok = true;
+  // f(i, values of four columns): the accumulator at d0, this thread's part
+  auto each4 = [&](uint32_t d0, auto f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(taddr + d0 + 32 * h, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        f(8 * h + i, make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                 __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+    }
+  };
+  ms_publish();
+  for (int k = 0; k < a.steps && ok; ++k) {
+    const bool last = k + 1 == a.steps;
+    // P = a I + b S + c S^2; the first Q is the first P
+    if (threadIdx.x == 0) {
+      ms_mma<false, false>(tmem, S[0], S[1], S[0], S[1], a.r16, a.r16);
+      mma_commit(&ctl->bar);
+    }
+    ok = ms_wait(ctl, phase, a.status);
+    if (!ok) break;
+    const float cs = a.c / (kMsSs * kMsSs);
+    each4(0, [&](int i, float4 d) {
+      float4 p;
+      p.x = fmaf(cs, d.x, a.b * s[i].x);
+      p.y = fmaf(cs, d.y, a.b * s[i].y);
+      p.z = fmaf(cs, d.z, a.b * s[i].z);
+      p.w = fmaf(cs, d.w, a.b * s[i].w);
+      const int col = c0 + 4 * i;
+      if (row < a.r) {
+        if (row == col) p.x += a.a;
+        if (row == col + 1) p.y += a.a;
+        if (row == col + 2) p.z += a.a;
+        if (row == col + 3) p.w += a.a;
+      }
+      put(p_hi, p_lo, i, p, kMsSp);
+      if (k == 0) put(q_hi, q_lo, i, p, a.sq);
+    });
+    ms_publish();
+    if (k == 0 && last) break;
+    // Q' = P Q and T = P S (into S's images, which are read by then)
+    if (threadIdx.x == 0) {
+      if (k > 0) ms_mma<false, false>(tmem, P[0], P[1], Q[0], Q[1], a.r16, a.r16);
+      if (!last) ms_mma<false, false>(tmem + 128, P[0], P[1], S[0], S[1], a.r16, a.r16);
+      mma_commit(&ctl->bar);
+    }
+    ok = ms_wait(ctl, phase, a.status);
+    if (!ok) break;
+    if (k > 0) each4(0, [&](int i, float4 d) { put(q_hi, q_lo, i, d, 1.f / kMsSp); });
+    if (last) break;
+    each4(128, [&](int i, float4 d) { put(s_hi, s_lo, i, d, kMsSt / (kMsSp * kMsSs)); });
+    ms_publish();
+    // S' = T P
+    if (threadIdx.x == 0) {
+      ms_mma<false, false>(tmem, S[0], S[1], P[0], P[1], a.r16, a.r16);
+      mma_commit(&ctl->bar);
+    }
+    ok = ms_wait(ctl, phase, a.status);
+    if (!ok) break;
+    each4(0, [&](int i, float4 d) {
+      const float f = 1.f / (kMsSt * kMsSp);
+      s[i] = make_float4(d.x * f, d.y * f, d.z * f, d.w * f);
+      put(s_hi, s_lo, i, s[i], kMsSs);
+    });
+    ms_publish();
+  }
+  __syncthreads();
+  // Q's images as they are, for the next kernel's bulk copies (rows past r16 are not read)
+  uint4* dst = reinterpret_cast<uint4*>(a.q + static_cast<int64_t>(g) * 2 * kMsImage);
+  for (int i = threadIdx.x; i < 2 * kMsImage / 16; i += kMsThreads)
+    if ((i * 16 % kMsBlock) / 128 < a.r16) dst[i] = *reinterpret_cast<const uint4*>(q_hi + 16 * i);
+  ms_end(tmem, 256);
+}
+
+// Grid (parts, groups).  X of a piece: Q times it (or it times Q), in fp32 through shared
+// memory to rows of 512 bytes, so that weights and results move whole row segments.
+template <typename T, bool VEC, bool OUT_VEC>
+__global__ void __launch_bounds__(kMsThreads) muon_apply_kernel(const __grid_constant__ MuonSmallArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* hi = ms_smem(smem_raw);
+  uint8_t *lo = hi + kMsImage, *q_hi = hi + 2 * kMsImage;
+  MsCtl* ctl = reinterpret_cast<MsCtl*>(hi + 4 * kMsImage);
+  const uint32_t tmem = ms_begin(ctl, 128);
+  pdl_wait();
+  pdl_trigger();
+  const int warp = warp_id(), lane = lane_id(), g = blockIdx.y;
+  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 64;
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(g) * 2 * kMsImage);
+  for (int i = threadIdx.x; i < 2 * kMsImage / 16; i += kMsThreads)
+    if ((i * 16 % kMsBlock) / 128 < a.r16) *reinterpret_cast<uint4*>(q_hi + 16 * i) = __ldg(src + i);
+  const double inv = a.inv_norm[g];
+  const int64_t base = static_cast<int64_t>(g) * a.rows * a.cols;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (int piece = blockIdx.x; piece < a.pieces && ok; piece += gridDim.x) {
+    float4 u[16];
+    ms_load<T, VEC, false>(a, g, piece, u);
+    const int e = ms_image(a, u, hi, lo, ctl->red);
+    ms_publish();
+    if (threadIdx.x == 0) {
+      const uint32_t h = smem_u32(hi), l = smem_u32(lo), qh = smem_u32(q_hi), ql = qh + kMsImage;
+      if (a.tall) ms_mma<false, false>(tmem, h, l, qh, ql, a.r16, a.r16);
+      else ms_mma<false, true>(tmem, qh, ql, h, l, 128, a.r16);
+      mma_commit(&ctl->bar);
+    }
+    const float f = static_cast<float>(inv * ldexp(1.0, -e));
+    ok = ms_wait(ctl, phase, a.status);
+    if (!ok) break;
+    const int r0 = a.tall ? piece * 128 : 0, n0 = a.tall ? 0 : piece * 128;
+    const int rows = min(128, a.rows - r0), cols = min(128, a.cols - n0);
+    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(taddr + 32 * h, v);
+      tmem_ld_wait();
+      if (row < rows && c0 + 32 * h < cols) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(hi + row * 512 + (((c0 + 32 * h) / 4 + i) ^ (row & 7)) * 16) =
+              make_float4(f * __uint_as_float(v[4 * i]), f * __uint_as_float(v[4 * i + 1]),
+                          f * __uint_as_float(v[4 * i + 2]), f * __uint_as_float(v[4 * i + 3]));
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    for (int i = warp; i < rows; i += kMsThreads / 32) {
+      const int col = 4 * lane;
+      if (col >= cols) continue;
+      const float4 x4 = *reinterpret_cast<const float4*>(hi + i * 512 + ((lane ^ (i & 7)) * 16));
+      float x[4] = {x4.x, x4.y, x4.z, x4.w};
+      const int64_t at = base + static_cast<int64_t>(r0 + i) * a.cols + n0 + col;
+      if constexpr (OUT_VEC) {
+        if (a.w) {
+          const float4 wv = load4<__nv_bfloat16>(a.w + at);
+          const float wf[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = fmaf(a.keep, wf[j], -a.step * x[j]);
+        }
+        *reinterpret_cast<uint2*>(a.out + at) = make_uint2(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col + j < cols) {
+            if (a.w) x[j] = fmaf(a.keep, __bfloat162float(a.w[at + j]), -a.step * x[j]);
+            a.out[at + j] = __float2bfloat16_rn(x[j]);
+          }
+      }
+    }
+    __syncthreads();  // the image is written again
+  }
+  ms_end(tmem, 128);
+}
+
+}  // namespace moe

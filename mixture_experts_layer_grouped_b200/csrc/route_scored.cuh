@@ -24,6 +24,7 @@
 namespace moe {
 
 constexpr int kRsWarps = 4;  // rows (warps) per block of the row kernels
+constexpr float kTinySum = 1e-30f;  // sums of sigmoids below this lose bits in 32
 
 struct ScoredArgs {
   const float* logits;    // [T, E] (when n_splits == 0)
@@ -34,6 +35,8 @@ struct ScoredArgs {
   int32_t* topk_idx;      // [T, k]
   float* topk_w;          // [T, k]
   int T, E, G, g, k, size;  // size = E / G
+  int lanes_per_group;    // size / PER where that is a power of two and whole, otherwise 0
+  int vec4;               // rows are whole 16-byte vectors
   uint32_t size_magic;    // ceil(2^32 / size): e / size == umulhi(e, magic) for e < 1024
   float rsf;
   int score, renorm, group_top;
@@ -43,9 +46,12 @@ __device__ __forceinline__ float exp_k(float x) { return expf(x); }
 __device__ __forceinline__ double exp_k(double x) { return exp(x); }
 
 // Order-preserving unsigned image of a key; 0 is below every key's and means "none".
+__device__ __forceinline__ uint32_t ordered_bits(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
 __device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);  // -0 and +0 are one key
-  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  return ordered_bits(v == 0.f ? 0.f : v);  // -0 and +0 are one key
 }
 __device__ __forceinline__ uint64_t ordered(double v) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v == 0.0 ? 0.0 : v));
@@ -55,13 +61,6 @@ __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-template <typename K> struct KeyOf;
-template <> struct KeyOf<float> { using U = uint32_t; };
-template <> struct KeyOf<double> { using U = uint64_t; };
-
-__device__ __forceinline__ uint32_t warp_max_key(uint32_t v) {
-  return __reduce_max_sync(0xffffffffu, v);
-}
 __device__ __forceinline__ uint64_t warp_max_key(uint64_t v) {
   const uint32_t hi = static_cast<uint32_t>(v >> 32);
   const uint32_t mh = __reduce_max_sync(0xffffffffu, hi);
@@ -111,106 +110,158 @@ __device__ __forceinline__ K selected_share(bool soft, bool have, float l) {
   return have ? w / s : K(0);
 }
 
-// One row by one warp; lane i holds the PER consecutive logits from i * PER on (-inf past
-// the last expert, and in place of a NaN).  Returns false, without having written
-// anything, when 32-bit keys cannot tell the selection (K = float only).
-template <int PER, typename K>
-__device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const float (&l)[PER],
-                                          const float* row, K* sh) {
-  using U = typename KeyOf<K>::U;
-  constexpr bool kFast = sizeof(K) == 4;
+// Groups kept, as a bit mask, given the two largest keys that each of `lpg` lanes of a group
+// has seen (lane / lpg is the group).  margin (or null): distance of the last kept group's
+// score from the first one left out, less the roundings of their keys (+inf: none is left out).
+template <typename K>
+__device__ __forceinline__ uint32_t keep_of_tops(const ScoredArgs& a, int lane, K m1, K m2, int lpg,
+                                                 float* margin) {
+  constexpr unsigned kAll = 0xffffffffu;
+  for (int o = 1; o < lpg; o <<= 1) {  // top 2 of two top-2 pairs
+    const K o1 = __shfl_xor_sync(kAll, m1, o);
+    const K o2 = __shfl_xor_sync(kAll, m2, o);
+    const K lo = m1 > o1 ? o1 : m1;
+    const K s2 = m2 > o2 ? m2 : o2;
+    m1 = m1 > o1 ? m1 : o1;
+    m2 = lo > s2 ? lo : s2;
+  }
+  K gs = m1;
+  float size = fabsf(float(m1));  // what the roundings of the score go by
+  if (a.group_top > 1 && m2 > K(-INFINITY)) {
+    gs += m2;
+    size += fabsf(float(m2));
+  }
+  gs = __shfl_sync(kAll, gs, (lane < a.G ? lane : 0) * lpg);
+  if (lane >= a.G) gs = K(-INFINITY);
+  int better = 0;
+  for (int o = 0; o < a.G; ++o) {
+    const K v = __shfl_sync(kAll, gs, o);
+    better += (v > gs || (v == gs && o < lane)) ? 1 : 0;
+  }
+  const bool some = gs > K(-INFINITY), kept = some && better < a.g;
+  if (margin) {
+    const uint32_t out = __reduce_max_sync(kAll, some && !kept ? ordered(float(gs)) : 0u);
+    const uint32_t in = __reduce_min_sync(kAll, kept ? ordered(float(gs)) : 0xFFFFFFFFu);
+    const uint32_t most = __reduce_max_sync(kAll, m1 > K(-INFINITY) ? __float_as_uint(size) : 0u);
+    if (out != 0u) *margin = unordered(in) - unordered(out) - 2.4e-7f * __uint_as_float(most);
+  }
+  return __ballot_sync(kAll, kept);
+}
+
+// Whether the lane's own group is kept, where every group is `lpg` whole neighbouring lanes
+// (a power of two) and m1, m2 are the images of the lane's two largest keys (0: none).  The
+// lanes of a group share the comparisons with the other groups.
+__device__ __forceinline__ bool own_group_kept(const ScoredArgs& a, int lane, uint32_t m1, uint32_t m2,
+                                               int lpg, bool want_margin, float* margin) {
+  constexpr unsigned kAll = 0xffffffffu;
+  for (int o = 1; o < lpg; o <<= 1) {
+    const uint32_t o1 = __shfl_xor_sync(kAll, m1, o);
+    const uint32_t o2 = __shfl_xor_sync(kAll, m2, o);
+    m2 = max(min(m1, o1), max(m2, o2));
+    m1 = max(m1, o1);
+  }
+  const int q = lane / lpg, sub = lane - q * lpg;
+  const bool some = m1 != 0u && q < a.G;
+  float gs = -INFINITY, size = 0.f;
+  if (some) {
+    gs = unordered(m1);
+    size = fabsf(gs);
+    if (a.group_top > 1 && m2 != 0u) {
+      gs += unordered(m2);
+      size += fabsf(unordered(m2));
+    }
+  }
+  int better = 0;
+  for (int o = sub; o < ((a.G + lpg - 1) & ~(lpg - 1)); o += lpg) {
+    const float v = __shfl_sync(kAll, gs, (o < a.G ? o : 0) * lpg);
+    better += o < a.G && (v > gs || (v == gs && o < q)) ? 1 : 0;
+  }
+  for (int o = 1; o < lpg; o <<= 1) better += __shfl_xor_sync(kAll, better, o);
+  const bool kept = some && better < a.g;
+  if (want_margin) {
+    const uint32_t out = __reduce_max_sync(kAll, some && !kept ? ordered(gs) : 0u);
+    const uint32_t in = __reduce_min_sync(kAll, kept ? ordered(gs) : 0xFFFFFFFFu);
+    const uint32_t most = __reduce_max_sync(kAll, __float_as_uint(size));
+    if (out != 0u) *margin = unordered(in) - unordered(out) - 2.4e-7f * __uint_as_float(most);
+  }
+  return kept;
+}
+
+// The same with the keys in shared memory: lpg lanes a group (one when G does not divide
+// 32), each scanning a strided share.
+template <typename F>
+__device__ __forceinline__ uint32_t kept_groups(const ScoredArgs& a, int lane, F key_of, float* margin) {
+  using K = decltype(key_of(0));
+  const int lpg = (32 % a.G == 0) ? 32 / a.G : 1;
+  const int q = lane / lpg, sub = lane - q * lpg;
+  K m1 = K(-INFINITY), m2 = K(-INFINITY);
+  if (q < a.G) {
+    for (int e = q * a.size + sub; e < (q + 1) * a.size; e += lpg) {
+      const K v = key_of(e);
+      if (v > m1) { m2 = m1; m1 = v; } else if (v > m2) { m2 = v; }
+    }
+  }
+  return keep_of_tops(a, lane, m1, m2, lpg, margin);
+}
+
+// One row in 64 bits by one warp, for the rows whose 32-bit keys do not tell the selection:
+// lane i holds the PER consecutive logits from i * PER on.  k rounds of a warp maximum.
+template <int PER>
+__device__ __noinline__ void route_row_64(const ScoredArgs& a, int t, const float* row, double* sh) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const bool biased = a.bias != nullptr;
   const bool by_score = a.G > 1 && !biased && a.group_top > 1;  // group sums of scores
   const bool soft = a.score == MOE_SCORE_SOFTMAX;
-  // the softmax's maximum and sum, where a score of a whole row is asked for
+  float l[PER];
   float lmax = -INFINITY;
-  K z = K(1), smax = K(1);
-  if (soft && (biased || by_score || !a.renorm)) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) lmax = fmaxf(lmax, l[i]);
-    lmax = warp_max_f(lmax);
-    K part = K(0);
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (l[i] > -INFINITY) part += exp_below<K>(l[i], lmax);
-    z = warp_sum(part);
-    smax = K(1) / z;
-  }
-  auto score_of = [&](float v) -> K {
-    return soft ? exp_below<K>(v, lmax) / z : sigmoid_k<K>(v);
-  };
-  U key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane * PER + i;
-    K v = K(-INFINITY);
-    if (l[i] > -INFINITY) {
-      v = K(l[i]);
-      if (biased) v = score_of(l[i]) + K(__ldg(a.bias + e));
-    }
-    key[i] = v > K(-INFINITY) ? ordered(v) : U(0);
-    if (a.G > 1 && e < a.E)
-      sh[e] = by_score ? (l[i] > -INFINITY ? score_of(l[i]) : K(-INFINITY))
-                       : (v > K(-INFINITY) ? v : K(-INFINITY));
+    const float v = e < a.E ? row[e] : -INFINITY;
+    l[i] = v > -INFINITY ? v : -INFINITY;  // NaN is masked like -inf
+    lmax = fmaxf(lmax, l[i]);
   }
-  // error of a 32-bit score, relative to the row's largest: the exponential's and the
-  // division's roundings, and for a softmax the sum's (PER + 5 additions)
-  const float eps_s = soft ? 8e-6f : 1e-6f;
+  lmax = warp_max_f(lmax);
+  double z = 1.0;
+  if (soft) {
+    z = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (l[i] > -INFINITY) z += exp_below<double>(l[i], lmax);
+    z = warp_sum(z);
+  }
+  auto score_of = [&](float v) -> double {
+    return soft ? exp_below<double>(v, lmax) / z : sigmoid_k<double>(v);
+  };
+  uint64_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane * PER + i;
+    double v = -INFINITY;
+    if (l[i] > -INFINITY) {
+      v = l[i];
+      if (biased) v = score_of(l[i]) + static_cast<double>(__ldg(a.bias + e));
+    }
+    key[i] = v > -INFINITY ? ordered(v) : 0ull;
+    if (a.G > 1 && e < a.E)
+      sh[e] = by_score ? (l[i] > -INFINITY ? score_of(l[i]) : -INFINITY) : (v > -INFINITY ? v : -INFINITY);
+  }
   if (a.G > 1) {
     __syncwarp();
-    // lpg lanes a group (one when G does not divide 32), each scanning a strided share
-    // for its two largest, merged by shuffles
-    const int lpg = (32 % a.G == 0) ? 32 / a.G : 1;
-    const int q = lane / lpg, sub = lane - q * lpg;
-    K m1 = K(-INFINITY), m2 = K(-INFINITY);
-    if (q < a.G) {
-      for (int e = q * a.size + sub; e < (q + 1) * a.size; e += lpg) {
-        const K v = sh[e];
-        if (v > m1) { m2 = m1; m1 = v; } else if (v > m2) { m2 = v; }
-      }
-    }
-    for (int o = 1; o < lpg; o <<= 1) {
-      const K o1 = __shfl_xor_sync(kAll, m1, o);
-      const K o2 = __shfl_xor_sync(kAll, m2, o);
-      const K lo = m1 > o1 ? o1 : m1;
-      const K s2 = m2 > o2 ? m2 : o2;
-      m1 = m1 > o1 ? m1 : o1;
-      m2 = lo > s2 ? lo : s2;
-    }
-    K gs = m1;
-    if (a.group_top > 1 && m2 > K(-INFINITY)) gs += m2;
-    gs = __shfl_sync(kAll, gs, (lane < a.G ? lane : 0) * lpg);
-    if (lane >= a.G) gs = K(-INFINITY);
-    int better = 0;
-    for (int o = 0; o < a.G; ++o) {
-      const K v = __shfl_sync(kAll, gs, o);
-      better += (v > gs || (v == gs && o < lane)) ? 1 : 0;
-    }
-    const bool some = gs > K(-INFINITY);
-    const bool kept = some && better < a.g;
-    const uint32_t keep = __ballot_sync(kAll, kept);
-    if (kFast && (biased || by_score)) {
-      const uint32_t out = __reduce_max_sync(kAll, some && !kept ? ordered(float(gs)) : 0u);
-      const uint32_t in = __reduce_min_sync(kAll, kept ? ordered(float(gs)) : 0xFFFFFFFFu);
-      if (out != 0u) {
-        const float lo = unordered(in), hi = unordered(out);
-        if (!(lo - hi > 2.f * eps_s * float(smax) + 2.4e-7f * (fabsf(lo) + fabsf(hi)))) return false;
-      }
-    }
+    const uint32_t keep = kept_groups(a, lane, [&](int e) { return sh[e]; }, nullptr);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const uint32_t e = static_cast<uint32_t>(lane * PER + i);
-      if (e >= static_cast<uint32_t>(a.E) || !((keep >> __umulhi(e, a.size_magic)) & 1u)) key[i] = U(0);
+      if (e >= static_cast<uint32_t>(a.E) || !((keep >> __umulhi(e, a.size_magic)) & 1u)) key[i] = 0ull;
     }
   }
   // the largest key left, the lowest expert among equal ones: experts ascend with the lane
   // and inside a lane, so the first lane of the ballot and its first maximum are the lowest
-  U mine = U(0);
+  uint64_t mine = 0ull;
   int at = 0;
   auto scan = [&]() {
-    mine = U(0);
+    mine = 0ull;
     at = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
@@ -218,93 +269,264 @@ __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const floa
   };
   scan();
   int sel = -1;
-  U sel_key = U(0), next = U(0);
-  const int rounds = a.k + ((kFast && biased) ? 1 : 0);
-  for (int r = 0; r < rounds; ++r) {
-    const U m = warp_max_key(mine);
-    if (m == U(0)) break;
-    if (r == a.k) { next = m; break; }
+  for (int r = 0; r < a.k; ++r) {
+    const uint64_t m = warp_max_key(mine);
+    if (m == 0ull) break;
     const int w = __ffs(__ballot_sync(kAll, mine == m)) - 1;
     const int e = __shfl_sync(kAll, lane * PER + at, w);
-    if (lane == r) { sel = e; sel_key = m; }
+    if (lane == r) sel = e;
     if (lane == w) {
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (i == at) key[i] = U(0);
+        if (i == at) key[i] = 0ull;
       scan();
     }
   }
-  if constexpr (kFast) {
-    if (biased) {
-      uint32_t below = __shfl_down_sync(kAll, sel_key, 1);
-      if (lane == a.k - 1 || lane == 31) below = next;
-      bool close = false;
-      if (lane < a.k && sel_key != 0u && below != 0u) {
-        const float hi = unordered(sel_key), lo = unordered(below);
-        close = !(hi - lo > eps_s * float(smax) + 1.2e-7f * (fabsf(hi) + fabsf(lo)));
-      }
-      if (__any_sync(kAll, close)) return false;
-    }
-  }
-  // gates: lane j has place j
   const bool have = lane < a.k && sel >= 0;
   const float lj = have ? row[sel] : -INFINITY;
-  K w = K(0);
-  if (a.renorm) w = selected_share<K>(soft, have, lj);
+  double w = 0.0;
+  if (a.renorm) w = selected_share<double>(soft, have, lj);
   else if (have) w = score_of(lj);
   if (lane < a.k) {
     a.topk_idx[static_cast<int64_t>(t) * a.k + lane] = sel;
-    a.topk_w[static_cast<int64_t>(t) * a.k + lane] = static_cast<float>(w * K(a.rsf));
+    a.topk_w[static_cast<int64_t>(t) * a.k + lane] = static_cast<float>(w * static_cast<double>(a.rsf));
+  }
+}
+
+// e^x and 1 / (1 + e^-x) from the hardware's approximations, for keys alone.  ex2.approx is
+// within 2^-22 of itself (and its argument's rounding adds |x| 2^-24), rcp.approx within 2^-23,
+// so a sigmoid is off by at most s (1 - s) (2^-22 + |x| 2^-24) + s (2^-23 + 2^-24) < 2.6e-7.
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + exp_fast(-x)));
+  return y;
+}
+
+constexpr int kRsCand = 64;  // candidates of a row
+
+// One row in 32 bits by one warp; lane i holds the PER consecutive logits from i * PER on
+// (-inf past the last expert, and in place of a NaN).  Returns false, without having written
+// anything, where 32-bit keys cannot tell the selection.
+//
+// Top k: the k-th largest of the lanes' maxima is at most the k-th largest key, so the keys
+// from it on are few (k and a few more) and hold the selection; they are gathered through
+// shared memory, one or two a lane, and each finds its rank by comparing itself to all.
+// That takes about half the instructions of k rounds of maximum and removal (and one round
+// more with a bias, whose next key the border check needs).
+template <int PER>
+__device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const float (&l)[PER],
+                                          const float (&bias)[PER], const float* row, float* sh) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const bool biased = a.bias != nullptr;
+  const bool by_score = a.G > 1 && !biased && a.group_top > 1;
+  const bool soft = a.score == MOE_SCORE_SOFTMAX;
+  // the softmax's maximum and sum, where a score of the whole row is asked for
+  float lmax = -INFINITY, z = 1.f, smax = 1.f;
+  if (soft && (biased || by_score || !a.renorm)) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) lmax = fmaxf(lmax, l[i]);
+    lmax = warp_max_f(lmax);
+    float part = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (l[i] > -INFINITY) part += l[i] == lmax ? 1.f : exp_fast(l[i] - lmax);
+    z = warp_sum(part);
+    smax = 1.f / z;
+  }
+  auto key_score = [&](float v) -> float {
+    return soft ? (v == lmax ? 1.f : exp_fast(v - lmax)) * smax : sigmoid_fast(v);
+  };
+  // error of such a score, doubled, relative to the row's largest: the exponential's and the
+  // division's roundings, and for a softmax the sum's (PER + 5 additions)
+  const float eps = (soft ? 8e-6f : 1e-6f) * smax;
+  uint32_t key[PER];
+  if (biased) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float v = key_score(l[i]) + bias[i];  // (a zero's sign is left to the border check)
+      key[i] = l[i] > -INFINITY && v > -INFINITY ? ordered_bits(v) : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = l[i] > -INFINITY ? ordered_bits(__fadd_rn(l[i], 0.f)) : 0u;
+  }
+  if (a.G > 1) {
+    float margin = INFINITY;
+    const int per_group = a.lanes_per_group;
+    if (per_group > 0) {  // a group is so many whole lanes, a power of two
+      uint32_t m1 = 0u, m2 = 0u;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        uint32_t v = key[i];
+        if (by_score) v = l[i] > -INFINITY ? ordered_bits(key_score(l[i])) : 0u;
+        m2 = max(m2, min(m1, v));
+        m1 = max(m1, v);
+      }
+      if (!own_group_kept(a, lane, m1, m2, per_group, biased || by_score, &margin)) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (lane * PER + i < a.E)
+          sh[lane * PER + i] = key[i] == 0u ? -INFINITY : (by_score ? key_score(l[i]) : unordered(key[i]));
+      __syncwarp();
+      const uint32_t keep = kept_groups(a, lane, [&](int e) { return sh[e]; }, &margin);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const uint32_t e = static_cast<uint32_t>(lane * PER + i);
+        if (e >= static_cast<uint32_t>(a.E) || !((keep >> __umulhi(e, a.size_magic)) & 1u)) key[i] = 0u;
+      }
+    }
+    if ((biased || by_score) && !(margin > 2.f * eps)) return false;
+  }
+  // a lower bound of the last key needed, from the lanes' maxima
+  const int need = a.k + (biased ? 1 : 0);
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) top = max(top, key[i]);
+  uint32_t bound = 1u;
+  for (int r = 0; r < need; ++r) {
+    const uint32_t m = __reduce_max_sync(kAll, top);
+    bound = max(m, 1u);
+    if (m == 0u) break;
+    const uint32_t who = __ballot_sync(kAll, top == m);
+    if (lane == __ffs(who) - 1) top = 0u;
+  }
+  // key and expert in one number: the larger key, or the lower expert, is the larger number
+  uint64_t* cand = reinterpret_cast<uint64_t*>(sh);
+  int mine_in = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) mine_in += key[i] >= bound ? 1 : 0;
+  int at = mine_in;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, at, o);
+    if (lane >= o) at += v;
+  }
+  const int n = __shfl_sync(kAll, at, 31);
+  if (n > kRsCand) return false;  // many equal keys
+  at -= mine_in;
+  if (mine_in > 0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (key[i] >= bound)
+        cand[at++] = (static_cast<uint64_t>(key[i]) << 32) | static_cast<uint32_t>(~(lane * PER + i));
+  }
+  __syncwarp();
+  uint64_t* sorted = cand + kRsCand;
+  for (int c = lane; c < n; c += 32) {
+    const uint64_t mine = cand[c];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += cand[j] > mine ? 1 : 0;
+    sorted[rank] = mine;
+  }
+  __syncwarp();
+  const uint64_t got = lane < min(n, a.k) ? sorted[lane] : 0ull;
+  const int sel = got != 0ull ? static_cast<int>(~static_cast<uint32_t>(got)) : -1;
+  if (biased) {
+    bool close = false;
+    if (sel >= 0 && lane + 1 < n) {
+      const float hi = unordered(static_cast<uint32_t>(got >> 32));
+      const float lo = unordered(static_cast<uint32_t>(sorted[lane + 1] >> 32));
+      close = !(hi - lo > eps + 1.2e-7f * (fabsf(hi) + fabsf(lo)));
+    }
+    if (__any_sync(kAll, close)) return false;
+  }
+  // gates: lane j has place j
+  const bool have = sel >= 0;
+  const float lj = have ? row[sel] : -INFINITY;
+  float w = 0.f;
+  if (have && !(soft && a.renorm)) w = soft ? exp_below<float>(lj, lmax) / z : sigmoid_k<float>(lj);
+  if (a.renorm) {
+    const float sum = soft ? 0.f : warp_sum(w);
+    if (sum >= kTinySum) w /= sum;
+    else w = selected_share<float>(soft, have, lj);
+  }
+  if (lane < a.k) {
+    a.topk_idx[static_cast<int64_t>(t) * a.k + lane] = sel;
+    a.topk_w[static_cast<int64_t>(t) * a.k + lane] = w * a.rsf;
   }
   return true;
 }
 
+// A warp per row, rows in a grid stride with the next row's logits on their way.
+// Floor: 4E bytes read a row (8k written); instruction issue is what it spends its time on.
 template <int PER>
-__device__ __noinline__ void route_row_64(const ScoredArgs& a, int t, const float* row, double* sh) {
-  const int lane = threadIdx.x & 31;
-  float l[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane * PER + i;
-    const float v = e < a.E ? row[e] : -INFINITY;
-    l[i] = v > -INFINITY ? v : -INFINITY;
-  }
-  route_row<PER, double>(a, t, l, row, sh);
-}
-
-// A warp per row.  Floor: 4E bytes read a row (8k written); the k rounds of two warp
-// reductions each are what it spends its issue slots on.
-template <int PER>
-__global__ void __launch_bounds__(kRsWarps * 32) route_scored_kernel(const __grid_constant__ ScoredArgs a) {
+__global__ void __launch_bounds__(kRsWarps * 32, PER <= 8 ? 8 : (PER <= 12 ? 6 : 1)) route_scored_kernel(const __grid_constant__ ScoredArgs a) {
   pdl_wait();
   pdl_trigger();
-  __shared__ double sh[kRsWarps][PER * 32];
+  // the fp32 row's group scores or candidates and their sorted copy, or the 64-bit row's scores
+  __shared__ double sh[kRsWarps][PER * 32 > 2 * kRsCand ? PER * 32 : 2 * kRsCand];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kRsWarps + w;
-  if (t >= a.T) return;
-  const int64_t at = static_cast<int64_t>(t) * a.E;
   const int64_t split_stride = static_cast<int64_t>(a.T) * a.E;
-  const float* row = (a.n_splits > 0 ? a.logits_out : a.logits) + at;
-  float l[PER];
+  const int stride = gridDim.x * kRsWarps;
+  float bias[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane * PER + i;
-    float v = -INFINITY;
-    if (e < a.E) {
-      if (a.n_splits > 0) {
-        v = a.partials[at + e];  // in split order, as route_select_kernel adds them
-        for (int sp = 1; sp < a.n_splits; ++sp) v += a.partials[sp * split_stride + at + e];
-        a.logits_out[at + e] = v;
-      } else {
-        v = row[e];
+    bias[i] = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+  }
+  auto fetch = [&](int t, float (&l)[PER]) {
+    const int64_t at = static_cast<int64_t>(t) * a.E;
+    const float* src = (a.n_splits > 0 ? a.partials : a.logits) + at;
+    if (PER % 4 == 0 && a.vec4) {
+#pragma unroll
+      for (int i = 0; i < PER; i += 4) {
+        const int e = lane * PER + i;
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (e < a.E) v = *reinterpret_cast<const float4*>(src + e);
+        l[i] = v.x;
+        l[i + 1] = v.y;
+        l[i + 2] = v.z;
+        l[i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = lane * PER + i;
+        l[i] = e < a.E ? src[e] : -INFINITY;
       }
     }
-    l[i] = v > -INFINITY ? v : -INFINITY;  // NaN is masked like -inf
-  }
-  __syncwarp();  // row[sel] below may be another lane's logits_out
-  if (!route_row<PER, float>(a, t, l, row, reinterpret_cast<float*>(sh[w]))) {
+    if (a.n_splits > 0) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = lane * PER + i;
+        if (e < a.E)  // in split order, as route_select_kernel adds them
+          for (int sp = 1; sp < a.n_splits; ++sp) l[i] += a.partials[sp * split_stride + at + e];
+      }
+    }
+  };
+  int t = blockIdx.x * kRsWarps + w;
+  float l[PER], next[PER];
+  if (t < a.T) fetch(t, l);
+  for (; t < a.T; t += stride) {
+    if (t + stride < a.T) fetch(t + stride, next);
+    const int64_t at = static_cast<int64_t>(t) * a.E;
+    const float* row = (a.n_splits > 0 ? a.logits_out : a.logits) + at;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = lane * PER + i;
+      if (a.n_splits > 0 && e < a.E) a.logits_out[at + e] = l[i];
+      l[i] = l[i] > -INFINITY ? l[i] : -INFINITY;  // NaN is masked like -inf
+    }
+    __syncwarp();  // row[sel] may be another lane's logits_out
+    if (!route_row<PER>(a, t, l, bias, row, reinterpret_cast<float*>(sh[w]))) {
+      __syncwarp();
+      route_row_64<PER>(a, t, row, sh[w]);
+    }
     __syncwarp();
-    route_row_64<PER>(a, t, row, sh[w]);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = next[i];
   }
 }
 
@@ -334,16 +556,79 @@ struct RouteBwdArgs {
   int score, renorm;
 };
 
+// Experts of a lane, in a row of 32 * PER: every 32nd one, or (VEC: rows of whole 16-byte
+// vectors) four neighbours in every 128.
+template <int PER, bool VEC>
+__device__ __forceinline__ int expert_of(int lane, int i) {
+  return VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : lane + 32 * i;
+}
+template <int PER, bool VEC>
+__device__ __forceinline__ void load_row(const float* row, int E, int lane, float fill, float (&v)[PER]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+      const int e = expert_of<PER, VEC>(lane, i);
+      float4 x = make_float4(fill, fill, fill, fill);
+      if (e < E) x = __ldg(reinterpret_cast<const float4*>(row + e));
+      v[i] = x.x;
+      v[i + 1] = x.y;
+      v[i + 2] = x.z;
+      v[i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = expert_of<PER, VEC>(lane, i);
+      v[i] = e < E ? __ldg(row + e) : fill;
+    }
+  }
+}
+
+// sigmoid(l) and 1 - sigmoid(l), each to its own precision: with q = exp(-|l|), 1 / (1 + q)
+// is the larger of the two and q / (1 + q) the smaller.
+__device__ __forceinline__ void sigmoid_both(float l, float& s, float& t) {
+  const float q = __expf(-fabsf(l)), r = __fdividef(1.f, 1.f + q);
+  s = l >= 0.f ? r : q * r;
+  t = l >= 0.f ? q * r : r;
+}
+
+// Scores of a row up to a common factor: l holds the logits (NaN: -inf) and becomes s; t gets
+// 1 - sigmoid (sigmoid only).  Returns the sum of s over the row, 0 where it is masked as a
+// whole; lmax: the logit whose s is 1, where s is e^(l - lmax) (shifted).
 // A row whose sigmoids sum to less than kTinySum has every logit below -69, where
-// sigmoid(l) = e^l to more than 32 bits: its shares are the softmax's.  Sets s to the
-// softmax's numerators, given the largest logit, and returns their sum (0 where the row is masked as a whole).
-constexpr float kTinySum = 1e-30f;
+// sigmoid(l) = e^l to more than 32 bits: its shares are the softmax's.
 template <int PER>
-__device__ __forceinline__ float tiny_sigmoid_row(const float (&l)[PER], float m, float (&s)[PER]) {
+__device__ __forceinline__ float scores_of_row(bool soft, float (&s)[PER], float (&t)[PER], float& lmax,
+                                               bool& shifted) {
   float z = 0.f;
+  lmax = -INFINITY;
+  shifted = soft;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    s[i] = l[i] > -INFINITY ? exp_below<float>(l[i], m) : 0.f;
+    s[i] = s[i] > -INFINITY ? s[i] : -INFINITY;
+    lmax = fmaxf(lmax, s[i]);
+  }
+  if (!soft) {
+    float v[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      sigmoid_both(s[i], v[i], t[i]);
+      if (!(s[i] > -INFINITY)) v[i] = 0.f;
+      z += v[i];
+    }
+    z = warp_sum(z);
+    if (z >= kTinySum) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) s[i] = v[i];
+      return z;
+    }
+    shifted = true;
+  }
+  lmax = warp_max_f(lmax);
+  z = 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    s[i] = s[i] > -INFINITY ? (s[i] == lmax ? 1.f : __expf(s[i] - lmax)) : 0.f;
     z += s[i];
   }
   return warp_sum(z);
@@ -361,7 +646,8 @@ __device__ __forceinline__ int sequence_of(const int32_t* off, int n_seq, int t)
   return lo;
 }
 
-template <int PER>
+// A warp per row.  Floor: 4E bytes read (where whole rows are needed) and 4E written a row.
+template <int PER, bool VEC>
 __global__ void __launch_bounds__(kRsWarps * 32) route_backward_kernel(const __grid_constant__ RouteBwdArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -372,94 +658,78 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_backward_kernel(const __g
   const int64_t base = static_cast<int64_t>(t) * a.E;
   const float* row = a.logits + base;
   const bool soft = a.score == MOE_SCORE_SOFTMAX;
+  // the selected places: lane j holds place j
+  int e = lane < a.k ? __ldg(a.topk_idx + static_cast<int64_t>(t) * a.k + lane) : -1;
+  const float dg = lane < a.k ? __ldg(a.dgate + static_cast<int64_t>(t) * a.k + lane) : 0.f;
   const int q = a.dscore ? sequence_of(a.seq_offsets, a.n_seq, t) : -1;
   const bool whole = q >= 0 || (soft && !a.renorm);  // scores of the whole row are needed
-  float l[PER];
+  float s[PER], t1[PER], c[PER];
   float lmax = -INFINITY, z = 0.f;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) l[i] = -INFINITY;
-  if (whole) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i;
-      const float v = e < a.E ? row[e] : -INFINITY;
-      l[i] = v > -INFINITY ? v : -INFINITY;
-      lmax = fmaxf(lmax, l[i]);
-    }
-    if (soft) lmax = warp_max_f(lmax);
-  }
-  // s of every expert this lane owns (softmax: numerators until z is known)
-  float s[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    s[i] = 0.f;
-    if (l[i] > -INFINITY) s[i] = soft ? exp_below<float>(l[i], lmax) : sigmoid_k<float>(l[i]);
-    z += s[i];
-  }
-  if (whole) z = warp_sum(z);
-  bool shifted = soft;  // s holds e^(l - lmax), not the scores themselves
-  if (whole && !soft && z < kTinySum) {
-    shifted = true;
-    lmax = warp_max_f(lmax);
-    z = tiny_sigmoid_row(l, lmax, s);
-  }
-  const float inv_z = z > 0.f ? 1.f / z : 0.f;
-  // the balance loss: c and sum c s'
+  bool shifted = soft;
   const float up = (q >= 0 && a.dloss) ? __ldg(a.dloss) : 1.f;
   const float* crow = a.dscore + static_cast<int64_t>(q >= 0 ? q : 0) * a.E;
-  float csum = 0.f;
+  if (whole) {
+    load_row<PER, VEC>(row, a.E, lane, -INFINITY, s);
+    if (q >= 0) load_row<PER, VEC>(crow, a.E, lane, 0.f, c);
+  }
+  float lj = -INFINITY;
+  if (e >= 0 && e < a.E) lj = __ldg(row + e);
+  const bool have = lj > -INFINITY;
+  if (!have) e = -1 - lane;  // no expert: equal to no other place
+  if (whole) z = scores_of_row<PER>(soft, s, t1, lmax, shifted);
+  const float inv_z = z > 0.f ? 1.f / z : 0.f;
+  float csum = 0.f;  // sum c s'
   if (q >= 0) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i;
-      if (e < a.E && s[i] > 0.f) csum = fmaf(up * __ldg(crow + e), s[i] * inv_z, csum);
+      c[i] *= up;
+      csum = fmaf(c[i], s[i], csum);
     }
-    csum = warp_sum(csum);
+    csum = warp_sum(csum) * inv_z;
   }
-  // the selected places: lane j holds place j; places that name the same expert add up
-  int e = lane < a.k ? __ldg(a.topk_idx + static_cast<int64_t>(t) * a.k + lane) : -1;
-  float lj = -INFINITY;
-  if (e >= 0 && e < a.E) lj = row[e];
-  const bool have = lj > -INFINITY;
-  if (!have) e = -1 - lane;  // no expert: equal to no other place
-  float g = have ? a.rsf * __ldg(a.dgate + static_cast<int64_t>(t) * a.k + lane) : 0.f;
+  float g = have ? a.rsf * dg : 0.f;
+  float sj = 0.f, tj = 0.f;  // the place's sigmoid and 1 - sigmoid
+  if (!soft && have) sigmoid_both(lj, sj, tj);
+  const float mine = shifted ? (have ? (lj == lmax ? 1.f : __expf(lj - lmax)) : 0.f) : sj;
   float w = 0.f;  // renormalised: the place's share; otherwise its score
   if (a.renorm) {
     w = selected_share<float>(soft, have, lj);
     const float gw = warp_sum(g * w);
     if (have) g -= gw;
   } else if (have) {
-    w = soft ? exp_below<float>(lj, lmax) * inv_z : sigmoid_k<float>(lj);
+    w = soft ? mine * inv_z : sj;
   }
   const float dot = (soft && !a.renorm) ? warp_sum(g * w) : 0.f;  // sum ds p
   // every expert of the row as if it were not selected
   float* out = a.dlogits ? a.dlogits + base : nullptr;
   __nv_bfloat16* brow = a.dense_b ? a.dense_b + static_cast<int64_t>(t) * a.ld_b + a.col_b : nullptr;
-  auto rest_of = [&](int ee, float lv, float sv) -> float {  // sv: sigmoid, or softmax's numerator
-    float d = 0.f;
-    if (lv > -INFINITY) {
-      const float c = q >= 0 ? up * __ldg(crow + ee) - csum : 0.f;
-      if (soft) {
-        if (whole) d = sv * inv_z * (c - dot);
-      } else if (q >= 0) {
-        d = sv * sigmoid_k<float>(-lv) * inv_z * c;
-      }
-    }
-    return d;
-  };
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int ee = lane + 32 * i;
-    const float d = ee < a.E ? rest_of(ee, l[i], s[i]) : 0.f;
-    if (out && ee < a.E) out[ee] = d;
-    if (brow && ee < a.ld_b - a.col_b) brow[ee] = __float2bfloat16_rn(d);
+    float d = 0.f;
+    if (whole) d = s[i] * inv_z * ((q >= 0 ? c[i] - csum : 0.f) - dot);
+    if (whole && !soft) d *= t1[i];
+    s[i] = d;
+  }
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+      const int ee = expert_of<PER, VEC>(lane, i);
+      if (out && ee < a.E) *reinterpret_cast<float4*>(out + ee) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int ee = expert_of<PER, VEC>(lane, i);
+    if (!VEC && out && ee < a.E) out[ee] = s[i];
+    if (brow && ee < a.ld_b - a.col_b) brow[ee] = __float2bfloat16_rn(ee < a.E ? s[i] : 0.f);
   }
   if (brow)
     for (int ee = lane + 32 * PER; ee < a.ld_b - a.col_b; ee += 32) brow[ee] = __float2bfloat16_rn(0.f);
-  // the selected ones over it (the warp's stores above come first)
+  // the selected ones over it (the warp's stores above come first); places that name the
+  // same expert add up
   const unsigned same = __match_any_sync(kAll, e);
   float gs = g;
-  if (__any_sync(kAll, have && (same & (same - 1)) != 0u)) {  // an expert named twice
+  if (__any_sync(kAll, have && (same & (same - 1)) != 0u)) {
     gs = 0.f;
     for (int j = 0; j < a.k; ++j) {
       const float o = __shfl_sync(kAll, g, j);
@@ -468,9 +738,10 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_backward_kernel(const __g
   }
   __syncwarp();
   if (have && (same & ((1u << lane) - 1u)) == 0u) {
-    const float sj = whole ? (shifted ? exp_below<float>(lj, lmax) : sigmoid_k<float>(lj)) : 0.f;
-    float d = rest_of(e, lj, sj);
-    d += soft ? gs * w : gs * w * sigmoid_k<float>(-lj);
+    float d = 0.f;
+    if (whole) d = mine * inv_z * ((q >= 0 ? up * __ldg(crow + e) - csum : 0.f) - dot);
+    d = fmaf(gs, w, d);
+    if (!soft) d *= tj;
     if (out) out[e] = d;
     if (brow) brow[e] = __float2bfloat16_rn(d);
   }
@@ -495,12 +766,12 @@ struct BalanceArgs {
   float* part;               // [tiles, E] sums of s' per tile
   int32_t* part_load;        // [tiles, E]
   int32_t* part_rows;        // [tiles]
-  double* seq_loss;          // [n_seq]
+  double* seq_loss;          // [n_seq, e_blocks]
   int32_t* done;             // [1]
   float* loss;               // [1]
   int32_t* load;             // [n_seq, E]
   float* dscore;             // [n_seq, E]
-  int T, E, k, n_seq, tiles, tile_rows;
+  int T, E, k, n_seq, tiles, tile_rows, e_blocks;
   float coef;
   int score;
 };
@@ -533,7 +804,8 @@ __device__ __forceinline__ int tiles_before(const BalanceArgs& a, int n, int* sh
   return s;
 }
 
-template <int PER>
+// Floor: 4E + 4k bytes read a row.  Each warp has the next row's logits on their way.
+template <int PER, bool VEC>
 __global__ void __launch_bounds__(kBalWarps * 32) balance_rows_kernel(const __grid_constant__ BalanceArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -584,43 +856,36 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_rows_kernel(const __gr
   for (int i = threadIdx.x; i < PER * 32; i += blockDim.x) hist[i] = 0;
   if (threadIdx.x == 0) rows_ok = 0;
   __syncthreads();
-  float acc[PER];
+  float acc[PER], s[PER], next[PER], t1[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
   int ok = 0;
-  for (int t = lo + w; t < hi; t += kBalWarps) {
-    const float* row = a.logits + static_cast<int64_t>(t) * a.E;
-    float l[PER], s[PER], m = -INFINITY, z = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i;
-      const float v = e < a.E ? row[e] : -INFINITY;
-      l[i] = v > -INFINITY ? v : -INFINITY;
-      m = fmaxf(m, l[i]);
-    }
-    const bool soft = a.score == MOE_SCORE_SOFTMAX;
-    if (soft) m = warp_max_f(m);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      s[i] = 0.f;
-      if (l[i] > -INFINITY) s[i] = soft ? exp_below<float>(l[i], m) : sigmoid_k<float>(l[i]);
-      z += s[i];
-    }
-    z = warp_sum(z);
-    if (!soft && z < kTinySum) z = tiny_sigmoid_row(l, warp_max_f(m), s);
+  const bool soft = a.score == MOE_SCORE_SOFTMAX;
+  int t = lo + w;
+  int pick = -1, pick_next = -1;
+  auto fetch = [&](int r, float (&v)[PER], int& p) {
+    load_row<PER, VEC>(a.logits + static_cast<int64_t>(r) * a.E, a.E, lane, -INFINITY, v);
+    p = lane < a.k ? __ldg(a.topk_idx + static_cast<int64_t>(r) * a.k + lane) : -1;
+  };
+  if (t < hi) fetch(t, s, pick);
+  for (; t < hi; t += kBalWarps) {
+    if (t + kBalWarps < hi) fetch(t + kBalWarps, next, pick_next);
+    float lmax;
+    bool shifted;
+    const float z = scores_of_row<PER>(soft, s, t1, lmax, shifted);
     if (z > 0.f) {
       const float inv = 1.f / z;
 #pragma unroll
       for (int i = 0; i < PER; ++i) acc[i] = fmaf(s[i], inv, acc[i]);
       ++ok;
     }
-    if (lane < a.k) {
-      const int e = __ldg(a.topk_idx + static_cast<int64_t>(t) * a.k + lane);
-      if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
-    }
+    if (pick >= 0 && pick < a.E) atomicAdd(&hist[pick], 1);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s[i] = next[i];
+    pick = pick_next;
   }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) sums[w][lane + 32 * i] = acc[i];
+  for (int i = 0; i < PER; ++i) sums[w][expert_of<PER, VEC>(lane, i)] = acc[i];
   if (lane == 0) atomicAdd(&rows_ok, ok);
   __syncthreads();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * a.E;
@@ -634,14 +899,18 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_rows_kernel(const __gr
   if (threadIdx.x == 0) a.part_rows[blockIdx.x] = rows_ok;
 }
 
-// A block per sequence; the last one to finish adds the sequences' losses in order.
-__global__ void __launch_bounds__(256) balance_finish_kernel(const __grid_constant__ BalanceArgs a) {
+// A block per sequence and 64 experts, eight threads an expert over the sequence's tiles; the
+// last block to finish adds the blocks' losses in order.
+constexpr int kBalExperts = 64, kBalSlices = 8;
+__global__ void __launch_bounds__(kBalExperts * kBalSlices) balance_finish_kernel(const __grid_constant__ BalanceArgs a) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int sh[8];
-  __shared__ double shd[8];
+  constexpr int kWarps = kBalExperts * kBalSlices / 32;
+  __shared__ int sh[kWarps];
+  __shared__ double shd[kBalSlices][kBalExperts];
+  __shared__ int shc[kBalSlices][kBalExperts];
   __shared__ int last;
-  const int q = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int q = blockIdx.x / a.e_blocks, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int first = a.seq_offsets ? tiles_before(a, q, sh) : 0;
   const int n = min(seq_tiles(a, q), max(a.tiles - first, 0));
   int rows = 0;
@@ -649,47 +918,56 @@ __global__ void __launch_bounds__(256) balance_finish_kernel(const __grid_consta
   rows = warp_sum(rows);
   __syncthreads();
   if (lane == 0) sh[w] = rows;
-  __syncthreads();
-  rows = 0;
-  for (int i = 0; i < 8; ++i) rows += sh[i];
-  const double inv_n = rows > 0 ? 1.0 / rows : 0.0;
-  double mine = 0.0;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    double p = 0.0;
-    int64_t c = 0;
-    for (int b = 0; b < n; ++b) {
+  const int el = threadIdx.x % kBalExperts, sl = threadIdx.x / kBalExperts;
+  const int e = (blockIdx.x - q * a.e_blocks) * kBalExperts + el;
+  double p = 0.0;
+  int c = 0;
+  if (e < a.E) {
+#pragma unroll 8
+    for (int b = sl; b < n; b += kBalSlices) {
       const int64_t at = static_cast<int64_t>(first + b) * a.E + e;
       p += a.part[at];
       c += a.part_load[at];
     }
-    const double d = static_cast<double>(a.coef) / a.n_seq * a.E / a.k * static_cast<double>(c) *
-                     inv_n * inv_n;
-    mine += d * p;
-    a.load[static_cast<int64_t>(q) * a.E + e] = static_cast<int32_t>(c);
-    a.dscore[static_cast<int64_t>(q) * a.E + e] = static_cast<float>(d);
   }
-  mine = warp_sum(mine);
-  if (lane == 0) shd[w] = mine;
+  shd[sl][el] = p;
+  shc[sl][el] = c;
+  __syncthreads();
+  rows = 0;
+  for (int i = 0; i < kWarps; ++i) rows += sh[i];
+  const double inv_n = rows > 0 ? 1.0 / rows : 0.0;
+  if (sl == 0) {
+    for (int i = 1; i < kBalSlices; ++i) {
+      p += shd[i][el];
+      c += shc[i][el];
+    }
+    const double d = static_cast<double>(a.coef) / a.n_seq * a.E / a.k * c * inv_n * inv_n;
+    if (e < a.E) {
+      a.load[static_cast<int64_t>(q) * a.E + e] = c;
+      a.dscore[static_cast<int64_t>(q) * a.E + e] = static_cast<float>(d);
+    }
+    shd[0][el] = d * p;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
     double v = 0.0;
-    for (int i = 0; i < 8; ++i) v += shd[i];
-    a.seq_loss[q] = v;
+    for (int i = 0; i < kBalExperts; ++i) v += shd[0][i];
+    a.seq_loss[blockIdx.x] = v;
     __threadfence();
-    last = atomicAdd(a.done, 1) == a.n_seq - 1;
+    last = atomicAdd(a.done, 1) == static_cast<int>(gridDim.x) - 1;
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
   double v = 0.0;
-  for (int i = threadIdx.x; i < a.n_seq; i += blockDim.x) v += __ldcg(a.seq_loss + i);
+  for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += blockDim.x) v += __ldcg(a.seq_loss + i);
   v = warp_sum(v);
   __syncthreads();
-  if (lane == 0) shd[w] = v;
+  if (lane == 0) shd[0][w] = v;
   __syncthreads();
   if (threadIdx.x == 0) {
     v = 0.0;
-    for (int i = 0; i < 8; ++i) v += shd[i];
+    for (int i = 0; i < kWarps; ++i) v += shd[0][i];
     *a.loss = static_cast<float>(v);
   }
 }

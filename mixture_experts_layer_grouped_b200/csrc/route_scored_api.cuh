@@ -51,9 +51,14 @@ moe_status do_route_scored(const moe_config& c, const moe_router& r, const void*
   a.score = r.score;
   a.renorm = r.renormalize;
   a.group_top = r.group_top;
+  a.vec4 = c.E % 4 == 0 && aligned16(a.n_splits > 0 ? a.partials : a.logits) ? 1 : 0;
   return by_experts(c.E, [&](auto per) -> moe_status {
-    MOE_TRY(launch_pdl(route_scored_kernel<decltype(per)::value>,
-                       dim3((c.T + kRsWarps - 1) / kRsWarps), dim3(kRsWarps * 32), 0, s, a));
+    constexpr int PER = decltype(per)::value;
+    const int lanes = a.size % PER == 0 ? a.size / PER : 0;
+    a.lanes_per_group = (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    const int want = (c.T + kRsWarps - 1) / kRsWarps, most = sm_count() * 8;
+    MOE_TRY(launch_pdl(route_scored_kernel<PER>, dim3(want < most ? want : most),
+                       dim3(kRsWarps * 32), 0, s, a));
     return launch_check();
   });
 }
@@ -89,9 +94,14 @@ moe_status do_route_backward(const moe_config& c, const moe_router& r, const flo
   a.rsf = c.routed_scaling_factor;
   a.score = r.score;
   a.renorm = r.renormalize;
+  const bool vec = c.E % 4 == 0 && aligned16(logits) && aligned16(dlogits) && aligned16(bal.dscore);
   return by_experts(c.E, [&](auto per) -> moe_status {
-    MOE_TRY(launch_pdl(route_backward_kernel<decltype(per)::value>,
-                       dim3((c.T + kRsWarps - 1) / kRsWarps), dim3(kRsWarps * 32), 0, s, a));
+    constexpr int PER = decltype(per)::value;
+    auto kern = route_backward_kernel<PER, false>;
+    if constexpr (PER % 4 == 0) {
+      if (vec) kern = route_backward_kernel<PER, true>;
+    }
+    MOE_TRY(launch_pdl(kern, dim3((c.T + kRsWarps - 1) / kRsWarps), dim3(kRsWarps * 32), 0, s, a));
     return launch_check();
   });
 }
@@ -118,7 +128,8 @@ BalanceLayout balance_layout(const moe_config& c, int32_t n_seq) {
   L.part = o; o = align_up(o + n);
   L.part_load = o; o = align_up(o + n);
   L.part_rows = o; o = align_up(o + static_cast<size_t>(L.tiles) * 4);
-  L.seq_loss = o; o = align_up(o + static_cast<size_t>(n_seq) * 8);
+  L.seq_loss = o;
+  o = align_up(o + static_cast<size_t>(n_seq) * ((c.E + kBalExperts - 1) / kBalExperts) * 8);
   L.done = o; o = align_up(o + 4);
   L.total = o;
   return L;
@@ -214,12 +225,19 @@ moe_status moe_balance_loss(const moe_config* cfg, const moe_router* router, con
   a.coef = coef;
   a.score = router->score;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool vec = cfg->E % 4 == 0 && aligned16(logits);
   MOE_TRY(by_experts(cfg->E, [&](auto per) -> moe_status {
-    MOE_TRY(launch_pdl(balance_rows_kernel<decltype(per)::value>, dim3(a.tiles),
-                       dim3(kBalWarps * 32), 0, s, a));
+    constexpr int PER = decltype(per)::value;
+    auto kern = balance_rows_kernel<PER, false>;
+    if constexpr (PER % 4 == 0) {
+      if (vec) kern = balance_rows_kernel<PER, true>;
+    }
+    MOE_TRY(launch_pdl(kern, dim3(a.tiles), dim3(kBalWarps * 32), 0, s, a));
     return launch_check();
   }));
-  MOE_TRY(launch_pdl(balance_finish_kernel, dim3(n_seq), dim3(256), 0, s, a));
+  a.e_blocks = (cfg->E + kBalExperts - 1) / kBalExperts;
+  MOE_TRY(launch_pdl(balance_finish_kernel, dim3(n_seq * a.e_blocks),
+                     dim3(kBalExperts * kBalSlices), 0, s, a));
   return launch_check();
 }
 

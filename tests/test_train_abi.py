@@ -127,9 +127,9 @@ def test_binding_checks_shapes_and_devices(M):
     x, idx, w = torch.zeros(T, E), torch.zeros(T, k, dtype=torch.int32), torch.zeros(T, k)
     with pytest.raises(ValueError):
         M.moe_route_scored(c, r, idx, w, logits_in=x)
-    with pytest.raises(ValueError, match="expected shape"):
+    with pytest.raises(ValueError, match="of shape"):
         M.moe_route_scored(c, r, idx, w, logits_in=x[:-1])
-    with pytest.raises(ValueError, match="expected shape"):
+    with pytest.raises(ValueError, match="of shape"):
         M.moe_route_backward(c, r, x[:, 1:], idx, w, x)
     with pytest.raises(ValueError, match="offsets"):
         M.moe_balance_loss(c, r, x, idx, 0.1, w, idx, w, x, seq_offsets=torch.zeros(1))
@@ -139,5 +139,5 @@ def test_binding_checks_shapes_and_devices(M):
         M.moe_orthogonalize(m, g, g, g)
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         M.moe_orthogonalize(m, g.half(), g, g)
-    with pytest.raises(ValueError, match="expected shape"):
+    with pytest.raises(ValueError, match="of shape"):
         M.moe_orthogonalize(m, g.mT, g, g)
