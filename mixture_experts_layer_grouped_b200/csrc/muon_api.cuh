@@ -64,7 +64,7 @@ bool muon_small(const moe_muon_config& c) {
 
 struct MuonSmallLayout {
   size_t status, part, part_exp, q, inv_norm, total;
-  int pieces, parts;
+  int pieces, gram_ctas;
 };
 
 MuonSmallLayout muon_small_layout(const moe_muon_config& c) {
@@ -72,14 +72,17 @@ MuonSmallLayout muon_small_layout(const moe_muon_config& c) {
   const size_t G = c.groups;
   const int n = c.rows > c.cols ? c.rows : c.cols;
   L.pieces = (n + 127) / 128;
-  // parts of a matrix's sum: enough CTAs for two rounds of the GPU, but one CTA adds them up
-  int parts = (2 * 148 + c.groups - 1) / c.groups;
-  if (parts > kMsMaxParts) parts = kMsMaxParts;
-  L.parts = parts < L.pieces ? parts : L.pieces;
+  // CTAs of the sums: one round of the GPU, at most kMsMaxParts a matrix (one CTA adds them up)
+  const int64_t units = static_cast<int64_t>(c.groups) * L.pieces;
+  int64_t ctas = static_cast<int64_t>(c.groups) * kMsMaxParts;
+  if (ctas > 148) ctas = 148;
+  if (ctas > units) ctas = units;
+  L.gram_ctas = static_cast<int>(ctas);
+  const size_t slots = G + L.gram_ctas;
   size_t o = 0;
   L.status = o; o = align_up(o + 4);
-  L.part = o; o = align_up(o + G * L.parts * 16 * kMsThreads * 16);
-  L.part_exp = o; o = align_up(o + G * L.parts * 4);
+  L.part = o; o = align_up(o + slots * 8 * kMsThreads * 16);
+  L.part_exp = o; o = align_up(o + slots * 4);
   L.q = o; o = align_up(o + G * 2 * kMsImage);
   L.inv_norm = o; o = align_up(o + G * 8);
   L.total = o;
@@ -336,7 +339,8 @@ moe_status muon_small_run(const moe_muon_config& c, const MuonArgs& u, void* ws,
   a.r = a.tall ? c.cols : c.rows;
   a.r16 = (a.r + 15) / 16 * 16;
   a.pieces = L.pieces;
-  a.parts = L.parts;
+  a.units = static_cast<int64_t>(c.groups) * L.pieces;
+  a.gram_ctas = L.gram_ctas;
   a.steps = c.steps;
   a.nesterov = u.nesterov ? 1 : 0;
   a.beta = u.beta;
@@ -350,10 +354,8 @@ moe_status muon_small_run(const moe_muon_config& c, const MuonArgs& u, void* ws,
   a.status = status_ptr(b);
   const bool vec = c.cols % 4 == 0 && aligned16(u.grad) && aligned16(u.mom_in) && aligned16(u.mom_out);
   const bool out_vec = c.cols % 4 == 0 && aligned16(u.out) && aligned16(u.w);
-  const dim3 grid(static_cast<unsigned>(L.parts), static_cast<unsigned>(c.groups));
-  int applies = (sm_count() + c.groups - 1) / c.groups;  // CTAs a matrix: one round of the GPU
-  if (applies > L.pieces) applies = L.pieces;
-  const dim3 agrid(static_cast<unsigned>(applies), static_cast<unsigned>(c.groups));
+  const dim3 grid(static_cast<unsigned>(L.gram_ctas));
+  const dim3 agrid(static_cast<unsigned>(a.units < sm_count() ? a.units : sm_count()));
   auto run = [&](auto gram, auto apply) -> moe_status {
     MOE_TRY(launch_ms(gram, grid, kMsGramSmem, s, a));
     MOE_TRY(launch_ms(muon_chain_kernel, dim3(c.groups), kMsChainSmem, s, a));

@@ -18,13 +18,16 @@
 #pragma once
 
 #include "muon.cuh"
+#include "route_scored.cuh"  // warp_sum
 
 namespace moe {
 
-constexpr int kMsThreads = 256;
+constexpr int kMsThreads = 512;
+constexpr int kMsWarps = kMsThreads / 32;
+constexpr int kMsSlots = 128 / kMsWarps;     // rows of a piece that a warp loads
 constexpr int kMsBlock = 128 * 128;          // bytes of 128 rows x 64 fp16
 constexpr int kMsImage = 2 * kMsBlock;       // 128 x 128 fp16: two such blocks
-constexpr int kMsMaxParts = 16;
+constexpr int kMsMaxParts = 16;              // CTAs that share a matrix's sum
 constexpr float kMsSs = 16384.f, kMsSp = 4096.f, kMsSt = 8192.f;  // scales of S, P, P S
 
 struct MuonSmallArgs {
@@ -33,11 +36,13 @@ struct MuonSmallArgs {
   float* mom_out;
   const __nv_bfloat16* w;   // or null: out = X
   __nv_bfloat16* out;
-  float4* part;             // [groups, parts, 16, 256]: the threads' 64 sums each
-  int32_t* part_exp;        // [groups, parts]: the sums are u u^T 2^(2 exp)
+  float4* part;             // [slots, 8, 512]: a CTA's sums of a matrix, 32 a thread
+  int32_t* part_exp;        // [slots]: the sums are u u^T 2^(2 exp)
   uint8_t* q;               // [groups, 2, kMsImage]: Q's shared-memory images, hi and lo
   double* inv_norm;         // [groups]: 1 / (|u|_F + eps), over Q's scale
-  int rows, cols, r, r16, pieces, parts, steps;  // r16: r rounded up to 16
+  int rows, cols, r, r16, pieces, steps;  // r16: r rounded up to 16
+  int64_t units;            // groups * pieces, dealt to the CTAs in equal runs
+  int gram_ctas;            // CTAs of the gram kernel
   int tall, nesterov;
   float beta, a, b, c, eps, keep, step, sq;      // sq: scale of Q
   int32_t* status;
@@ -52,7 +57,22 @@ __device__ __forceinline__ float pow2f(int e) {  // 2^e, e in [-126, 127]
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// Four neighbouring fp32 values as hi and lo parts of an image pair.
+// Eight neighbouring fp32 values as hi and lo parts of an image pair.
+__device__ __forceinline__ void ms_store8(uint8_t* hi, uint8_t* lo, int row, int col, const float (&v)[8]) {
+  uint4 h4, l4;
+  __half2* h = reinterpret_cast<__half2*>(&h4);
+  __half2* l = reinterpret_cast<__half2*>(&l4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    const float2 f = __half22float2(h[i]);
+    l[i] = __floats2half2_rn(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+  }
+  const int at = ms_at(row, col);
+  *reinterpret_cast<uint4*>(hi + at) = h4;
+  *reinterpret_cast<uint4*>(lo + at) = l4;
+}
+// Four of them.
 __device__ __forceinline__ void ms_store4(uint8_t* hi, uint8_t* lo, int row, int col, float4 v) {
   const __half2 h0 = __floats2half2_rn(v.x, v.y), h1 = __floats2half2_rn(v.z, v.w);
   const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
@@ -84,10 +104,15 @@ __device__ __forceinline__ void ms_mma(uint32_t d, uint32_t a_hi, uint32_t a_lo,
   }
 }
 
-// u of a 128 x 128 piece, 16 rows a warp and four columns a lane; FIRST: the momentum is
-// formed and written, otherwise it is read back.
+// What u of a 128 x 128 piece is made of, eight rows a warp and four columns a lane: asked for
+// here, used by ms_form, so that a piece's loads run beside the one before it.  FIRST: the
+// momentum is formed and written, otherwise it is read back.
+struct MsRaw {
+  float4 g[kMsSlots], m[kMsSlots];
+};
+
 template <typename T, bool VEC, bool FIRST>
-__device__ __forceinline__ void ms_load(const MuonSmallArgs& a, int g, int piece, float4 (&u)[16]) {
+__device__ __forceinline__ void ms_load(const MuonSmallArgs& a, int g, int piece, MsRaw& u) {
   const int warp = warp_id(), lane = lane_id();
   const int r0 = a.tall ? piece * 128 : 0, c0 = a.tall ? 0 : piece * 128;
   const int64_t base = static_cast<int64_t>(g) * a.rows * a.cols;
@@ -96,19 +121,18 @@ __device__ __forceinline__ void ms_load(const MuonSmallArgs& a, int g, int piece
   const bool need_g = FIRST || !mom || a.nesterov;
   const int col = c0 + 4 * lane;
   const int r_end = min(a.rows, r0 + 128);
-  float4 m[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int row = r0 + warp + 8 * i;
-    u[i] = m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kMsSlots; ++i) {
+    const int row = r0 + warp + kMsWarps * i;
+    u.g[i] = u.m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row >= r_end || col >= a.cols) continue;
     const int64_t at = static_cast<int64_t>(row) * a.cols + col;
     if constexpr (VEC) {
-      if (need_g) u[i] = load4<T>(grad + at);
-      if (mom) m[i] = *reinterpret_cast<const float4*>(mom + base + at);
+      if (need_g) u.g[i] = load4<T>(grad + at);
+      if (mom) u.m[i] = *reinterpret_cast<const float4*>(mom + base + at);
     } else {
-      float* up = &u[i].x;
-      float* mp = &m[i].x;
+      float* up = &u.g[i].x;
+      float* mp = &u.m[i].x;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (col + j < a.cols) {
@@ -117,12 +141,22 @@ __device__ __forceinline__ void ms_load(const MuonSmallArgs& a, int g, int piece
         }
     }
   }
-  if (!mom) return;
+}
+
+// u in place of the gradient; FIRST: the new momentum goes out.
+template <bool VEC, bool FIRST>
+__device__ __forceinline__ void ms_form(const MuonSmallArgs& a, int g, int piece, MsRaw& u) {
+  if (!a.mom_in) return;
+  const int warp = warp_id(), lane = lane_id();
+  const int r0 = a.tall ? piece * 128 : 0, c0 = a.tall ? 0 : piece * 128;
+  const int64_t base = static_cast<int64_t>(g) * a.rows * a.cols;
+  const int col = c0 + 4 * lane;
+  const int r_end = min(a.rows, r0 + 128);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int row = r0 + warp + 8 * i;
-    float* up = &u[i].x;
-    float* mp = &m[i].x;
+  for (int i = 0; i < kMsSlots; ++i) {
+    const int row = r0 + warp + kMsWarps * i;
+    float* up = &u.g[i].x;
+    float* mp = &u.m[i].x;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (FIRST) mp[j] = fmaf(a.beta, mp[j], up[j]);
@@ -131,7 +165,7 @@ __device__ __forceinline__ void ms_load(const MuonSmallArgs& a, int g, int piece
     if (FIRST && row < r_end && col < a.cols) {
       const int64_t at = base + static_cast<int64_t>(row) * a.cols + col;
       if constexpr (VEC) {
-        *reinterpret_cast<float4*>(a.mom_out + at) = m[i];
+        *reinterpret_cast<float4*>(a.mom_out + at) = u.m[i];
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -143,12 +177,12 @@ __device__ __forceinline__ void ms_load(const MuonSmallArgs& a, int g, int piece
 
 // The piece's image pair, scaled so that its largest value is in [2^13, 2^14); returns the
 // exponent of the scale.  Rows past what the products read are left out.
-__device__ __forceinline__ int ms_image(const MuonSmallArgs& a, float4 (&u)[16], uint8_t* hi, uint8_t* lo,
+__device__ __forceinline__ int ms_image(const MuonSmallArgs& a, const float4 (&u)[kMsSlots], uint8_t* hi, uint8_t* lo,
                                         float* red) {
   const int warp = warp_id(), lane = lane_id();
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < kMsSlots; ++i)
     m = fmaxf(fmaxf(fmaxf(m, fabsf(u[i].x)), fmaxf(fabsf(u[i].y), fabsf(u[i].z))), fabsf(u[i].w));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -156,15 +190,15 @@ __device__ __forceinline__ int ms_image(const MuonSmallArgs& a, float4 (&u)[16],
   __syncthreads();
   m = red[0];
 #pragma unroll
-  for (int i = 1; i < kMsThreads / 32; ++i) m = fmaxf(m, red[i]);
+  for (int i = 1; i < kMsWarps; ++i) m = fmaxf(m, red[i]);
   // exponent of the largest value (an infinity or zero: no scale; far below fp32: clamped)
   const int em = static_cast<int>(__float_as_uint(m) >> 23) - 127;
   const int e = (m == 0.f || em == 128) ? 0 : min(13 - em, 126);
   const float s = pow2f(max(e, -126));
   const int rows = a.tall ? 128 : a.r16;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int row = warp + 8 * i;
+  for (int i = 0; i < kMsSlots; ++i) {
+    const int row = warp + kMsWarps * i;
     if (row >= rows) break;
     ms_store4(hi, lo, row, 4 * lane, make_float4(u[i].x * s, u[i].y * s, u[i].z * s, u[i].w * s));
   }
@@ -176,7 +210,7 @@ struct MsCtl {
   uint64_t bar;
   uint32_t tmem;
   int abort;
-  float red[kMsThreads / 32];
+  float red[kMsWarps];
 };
 
 __device__ __forceinline__ uint32_t ms_begin(MsCtl* ctl, uint32_t cols) {
@@ -227,9 +261,15 @@ __device__ __forceinline__ uint8_t* ms_smem(uint8_t* raw) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
 }
 
-// Grid (parts, groups): part p of a matrix takes pieces p, p + parts, ...
+// The units (matrix, piece) of CTA b of n: equal runs.
+__device__ __forceinline__ int64_t ms_first(const MuonSmallArgs& a, int b, int n) {
+  return a.units * b / n;
+}
+
+// A CTA takes a run of units; for each matrix that it meets it leaves its sums in slot
+// (CTA + matrix), which no other pair has.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kMsThreads) muon_gram_kernel(const __grid_constant__ MuonSmallArgs a) {
+__global__ void __launch_bounds__(kMsThreads, 1) muon_gram_kernel(const __grid_constant__ MuonSmallArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* hi = ms_smem(smem_raw);
   uint8_t* lo = hi + kMsImage;
@@ -237,18 +277,21 @@ __global__ void __launch_bounds__(kMsThreads) muon_gram_kernel(const __grid_cons
   const uint32_t tmem = ms_begin(ctl, 128);
   pdl_wait();
   pdl_trigger();
-  const int warp = warp_id(), lane = lane_id(), g = blockIdx.y;
-  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 64;
-  float acc[64];
-#pragma unroll
-  for (int j = 0; j < 64; ++j) acc[j] = 0.f;
+  const int warp = warp_id(), lane = lane_id();
+  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 32;
+  const int64_t u0 = ms_first(a, blockIdx.x, a.gram_ctas), u1 = ms_first(a, blockIdx.x + 1, a.gram_ctas);
+  float acc[32];
   int exp = 0;
-  bool first = true, ok = true;
   uint32_t phase = 0;
-  for (int piece = blockIdx.x; piece < a.pieces && ok; piece += a.parts) {
-    float4 u[16];
-    ms_load<T, VEC, true>(a, g, piece, u);
-    const int e = ms_image(a, u, hi, lo, ctl->red);
+  MsRaw u;
+  int g = static_cast<int>(u0 / a.pieces), piece = static_cast<int>(u0 - static_cast<int64_t>(g) * a.pieces);
+  bool first = true;
+  if (u0 < u1) ms_load<T, VEC, true>(a, g, piece, u);
+  for (int64_t v = u0; v < u1; ++v) {
+    ms_form<VEC, true>(a, g, piece, u);
+    const int e = ms_image(a, u.g, hi, lo, ctl->red);
+    const int g_next = piece + 1 == a.pieces ? g + 1 : g, p_next = piece + 1 == a.pieces ? 0 : piece + 1;
+    if (v + 1 < u1) ms_load<T, VEC, true>(a, g_next, p_next, u);
     ms_publish();
     if (threadIdx.x == 0) {
       const uint32_t h = smem_u32(hi), l = smem_u32(lo);
@@ -256,8 +299,7 @@ __global__ void __launch_bounds__(kMsThreads) muon_gram_kernel(const __grid_cons
       else ms_mma<false, false>(tmem, h, l, h, l, a.r16, 128);
       mma_commit(&ctl->bar);
     }
-    ok = ms_wait(ctl, phase, a.status);
-    if (!ok) break;
+    if (!ms_wait(ctl, phase, a.status)) break;
     // the sums keep the smaller exponent: what has the larger one is scaled down
     float f_acc = 1.f, f_new = 1.f;
     if (first) {
@@ -268,35 +310,42 @@ __global__ void __launch_bounds__(kMsThreads) muon_gram_kernel(const __grid_cons
     } else {
       f_new = 2 * (exp - e) < -126 ? 0.f : pow2f(2 * (exp - e));
     }
-    first = false;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
+    uint32_t d[32];
+    tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, d);
+    tmem_ld_wait();
+    if (first) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t v[32];
-      tmem_ld_32x32b_x32(taddr + 32 * h, v);
-      tmem_ld_wait();
+      for (int j = 0; j < 32; ++j) acc[j] = __uint_as_float(d[j]);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        acc[32 * h + j] = fmaf(__uint_as_float(v[j]), f_new, acc[32 * h + j] * f_acc);
+      for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(d[j]), f_new, acc[j] * f_acc);
     }
+    first = false;
+    if (g_next != g || v + 1 == u1) {
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) + g;
+      float4* dst = a.part + slot * (8 * kMsThreads) + threadIdx.x;
+      if (row < a.r16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c0 + 4 * i < a.r16)
+            dst[i * kMsThreads] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+      }
+      if (threadIdx.x == 0) a.part_exp[slot] = exp;
+      first = true;
+    }
+    g = g_next;
+    piece = p_next;
     tc_fence_before();
     __syncthreads();  // images and TMEM may be written again
     tc_fence_after();
   }
-  const int64_t slot = static_cast<int64_t>(g) * a.parts + blockIdx.x;
-  if (row < a.r16) {
-    float4* dst = a.part + slot * 16 * kMsThreads + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c0 + 4 * i < a.r16) dst[i * kMsThreads] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-  }
-  if (threadIdx.x == 0) a.part_exp[slot] = exp;
   ms_end(tmem, 128);
 }
 
-// One CTA a matrix.  A thread holds half a row of S in fp32; P, Q and S (or P S) live in
-// shared memory as image pairs.  Three dependent products a step, about 1 us each.
-__global__ void __launch_bounds__(kMsThreads) muon_chain_kernel(const __grid_constant__ MuonSmallArgs a) {
+// One CTA a matrix.  A thread holds a quarter of a row of S in fp32; P, Q and S (or P S) live
+// in shared memory as image pairs.  Three dependent products a step: at r = 128 each reads
+// 192 KB of shared memory (1536 clk of its bandwidth) and 256 KB of new images are written.
+__global__ void __launch_bounds__(kMsThreads, 1) muon_chain_kernel(const __grid_constant__ MuonSmallArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = ms_smem(smem_raw);
   uint8_t *s_hi = base, *s_lo = base + kMsImage, *p_hi = base + 2 * kMsImage, *p_lo = base + 3 * kMsImage,
@@ -306,107 +355,100 @@ __global__ void __launch_bounds__(kMsThreads) muon_chain_kernel(const __grid_con
   pdl_wait();
   pdl_trigger();
   const int warp = warp_id(), lane = lane_id(), g = blockIdx.x;
-  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 64;
+  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 32;
   const bool mine = row < a.r16 && c0 < a.r16;
-  const int vecs = mine ? min(16, (a.r16 - c0) / 4) : 0;  // of four columns
-  // S: the parts under one exponent
+  const bool warp_mine = (warp & 3) * 32 < a.r16 && c0 < a.r16;  // (TMEM loads are whole warps')
+  const int vecs = mine ? min(4, (a.r16 - c0) / 8) : 0;  // of eight columns
+  // S: the CTAs' sums under one exponent.  CTA b met this matrix if its run does.
+  const int64_t v0 = static_cast<int64_t>(g) * a.pieces, v1 = v0 + a.pieces;
+  int b0 = static_cast<int>(v0 * a.gram_ctas / a.units), b1 = static_cast<int>(v1 * a.gram_ctas / a.units);
+  while (b0 > 0 && ms_first(a, b0, a.gram_ctas) > v0) --b0;
+  while (ms_first(a, b0 + 1, a.gram_ctas) <= v0) ++b0;
+  while (b1 < a.gram_ctas && ms_first(a, b1, a.gram_ctas) < v1) ++b1;
+  while (b1 > b0 + 1 && ms_first(a, b1 - 1, a.gram_ctas) >= v1) --b1;
   int exp = 126;
-  for (int p = 0; p < a.parts; ++p) exp = min(exp, __ldg(a.part_exp + g * a.parts + p));
-  float4 s[16];
+  for (int b = b0; b < b1; ++b) exp = min(exp, __ldg(a.part_exp + b + g));
+  float s[32];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = 0; p < a.parts; ++p) {
-    const int64_t slot = static_cast<int64_t>(g) * a.parts + p;
+  for (int i = 0; i < 32; ++i) s[i] = 0.f;
+#pragma unroll 2
+  for (int b = b0; b < b1; ++b) {
+    const int64_t slot = static_cast<int64_t>(b) + g;
     const int d = 2 * (exp - __ldg(a.part_exp + slot));
     const float f = d < -126 ? 0.f : pow2f(d);
-    const float4* src = a.part + slot * 16 * kMsThreads + threadIdx.x;
+    const float4* src = a.part + slot * (8 * kMsThreads) + threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < vecs) {
+    for (int i = 0; i < 8; ++i)
+      if (i < 2 * vecs) {
         const float4 v = __ldg(src + i * kMsThreads);
-        s[i].x = fmaf(v.x, f, s[i].x);
-        s[i].y = fmaf(v.y, f, s[i].y);
-        s[i].z = fmaf(v.z, f, s[i].z);
-        s[i].w = fmaf(v.w, f, s[i].w);
+        s[4 * i] = fmaf(v.x, f, s[4 * i]);
+        s[4 * i + 1] = fmaf(v.y, f, s[4 * i + 1]);
+        s[4 * i + 2] = fmaf(v.z, f, s[4 * i + 2]);
+        s[4 * i + 3] = fmaf(v.w, f, s[4 * i + 3]);
       }
   }
-  // |u|^2 2^(2 exp) is the trace
+  // |u|^2 2^(2 exp) is the trace; the row's diagonal entry is the lane-th column of its quarter
   float diag = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (row == c0 + 4 * i) diag = s[i].x;
-    if (row == c0 + 4 * i + 1) diag = s[i].y;
-    if (row == c0 + 4 * i + 2) diag = s[i].z;
-    if (row == c0 + 4 * i + 3) diag = s[i].w;
-  }
-  if (!mine) diag = 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) diag += __shfl_xor_sync(0xffffffffu, diag, o);
+  for (int i = 0; i < 32; ++i)
+    if (lane == i) diag = s[i];
+  if (!mine || (warp >> 2) != (warp & 3)) diag = 0.f;
+  diag = warp_sum(diag);
   if (lane == 0) ctl->red[warp] = diag;
   __syncthreads();
   double trace = 0.0;
-  for (int i = 0; i < kMsThreads / 32; ++i) trace += ctl->red[i];
+  for (int i = 0; i < kMsWarps; ++i) trace += ctl->red[i];
   const double up = ldexp(1.0, -exp);
   const double inv = 1.0 / (sqrt(trace) * up + a.eps);
   if (threadIdx.x == 0) a.inv_norm[g] = inv / a.sq;
   const float f0 = static_cast<float>(up * inv);  // (its square may be past fp32)
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    s[i].x = s[i].x * f0 * f0;
-    s[i].y = s[i].y * f0 * f0;
-    s[i].z = s[i].z * f0 * f0;
-    s[i].w = s[i].w * f0 * f0;
-  }
-  auto put = [&](uint8_t* hi, uint8_t* lo, int i, float4 v, float f) {
-    if (i < vecs) ms_store4(hi, lo, row, c0 + 4 * i, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-  };
-#pragma unroll
-  for (int i = 0; i < 16; ++i) put(s_hi, s_lo, i, s[i], kMsSs);
   const uint32_t S[2] = {smem_u32(s_hi), smem_u32(s_lo)}, P[2] = {smem_u32(p_hi), smem_u32(p_lo)},
                  Q[2] = {smem_u32(q_hi), smem_u32(q_lo)};
   const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
-  uint32_t phase = 0;
-  bool ok = true;
-  // f(i, values of four columns): the accumulator at d0, this thread's part
-  auto each4 = [&](uint32_t d0, auto f) {
+  auto put = [&](uint8_t* hi, uint8_t* lo, const float (&v)[32], float f) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t v[32];
-      tmem_ld_32x32b_x32(taddr + d0 + 32 * h, v);
-      tmem_ld_wait();
+    for (int i = 0; i < 4; ++i) {
+      if (i >= vecs) break;
+      float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        f(8 * h + i, make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                 __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+      for (int j = 0; j < 8; ++j) x[j] = v[8 * i + j] * f;
+      ms_store8(hi, lo, row, c0 + 8 * i, x);
     }
   };
+  auto read = [&](uint32_t col, float (&v)[32]) {  // this thread's part of the accumulator there
+    uint32_t d[32];
+    tmem_ld_32x32b_x32(taddr + col, d);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]);
+  };
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s[i] = s[i] * f0 * f0;
+  put(s_hi, s_lo, s, kMsSs);
+  uint32_t phase = 0;
   ms_publish();
-  for (int k = 0; k < a.steps && ok; ++k) {
+  for (int k = 0; k < a.steps; ++k) {
     const bool last = k + 1 == a.steps;
+    float v[32];
     // P = a I + b S + c S^2; the first Q is the first P
     if (threadIdx.x == 0) {
       ms_mma<false, false>(tmem, S[0], S[1], S[0], S[1], a.r16, a.r16);
       mma_commit(&ctl->bar);
     }
-    ok = ms_wait(ctl, phase, a.status);
-    if (!ok) break;
-    const float cs = a.c / (kMsSs * kMsSs);
-    each4(0, [&](int i, float4 d) {
-      float4 p;
-      p.x = fmaf(cs, d.x, a.b * s[i].x);
-      p.y = fmaf(cs, d.y, a.b * s[i].y);
-      p.z = fmaf(cs, d.z, a.b * s[i].z);
-      p.w = fmaf(cs, d.w, a.b * s[i].w);
-      const int col = c0 + 4 * i;
-      if (row < a.r) {
-        if (row == col) p.x += a.a;
-        if (row == col + 1) p.y += a.a;
-        if (row == col + 2) p.z += a.a;
-        if (row == col + 3) p.w += a.a;
+    if (!ms_wait(ctl, phase, a.status)) break;
+    if (warp_mine) {
+      read(0, v);
+      const float cs = a.c / (kMsSs * kMsSs);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = fmaf(cs, v[i], a.b * s[i]);
+      if ((warp >> 2) == (warp & 3) && row < a.r) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (lane == i) v[i] += a.a;
       }
-      put(p_hi, p_lo, i, p, kMsSp);
-      if (k == 0) put(q_hi, q_lo, i, p, a.sq);
-    });
+      put(p_hi, p_lo, v, kMsSp);
+      if (k == 0) put(q_hi, q_lo, v, a.sq);
+    }
     ms_publish();
     if (k == 0 && last) break;
     // Q' = P Q and T = P S (into S's images, which are read by then)
@@ -415,38 +457,44 @@ __global__ void __launch_bounds__(kMsThreads) muon_chain_kernel(const __grid_con
       if (!last) ms_mma<false, false>(tmem + 128, P[0], P[1], S[0], S[1], a.r16, a.r16);
       mma_commit(&ctl->bar);
     }
-    ok = ms_wait(ctl, phase, a.status);
-    if (!ok) break;
-    if (k > 0) each4(0, [&](int i, float4 d) { put(q_hi, q_lo, i, d, 1.f / kMsSp); });
+    if (!ms_wait(ctl, phase, a.status)) break;
+    if (warp_mine && k > 0) {
+      read(0, v);
+      put(q_hi, q_lo, v, 1.f / kMsSp);
+    }
     if (last) break;
-    each4(128, [&](int i, float4 d) { put(s_hi, s_lo, i, d, kMsSt / (kMsSp * kMsSs)); });
+    if (warp_mine) {
+      read(128, v);
+      put(s_hi, s_lo, v, kMsSt / (kMsSp * kMsSs));
+    }
     ms_publish();
     // S' = T P
     if (threadIdx.x == 0) {
       ms_mma<false, false>(tmem, S[0], S[1], P[0], P[1], a.r16, a.r16);
       mma_commit(&ctl->bar);
     }
-    ok = ms_wait(ctl, phase, a.status);
-    if (!ok) break;
-    each4(0, [&](int i, float4 d) {
-      const float f = 1.f / (kMsSt * kMsSp);
-      s[i] = make_float4(d.x * f, d.y * f, d.z * f, d.w * f);
-      put(s_hi, s_lo, i, s[i], kMsSs);
-    });
+    if (!ms_wait(ctl, phase, a.status)) break;
+    if (warp_mine) {
+      read(0, s);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] *= 1.f / (kMsSt * kMsSp);
+      put(s_hi, s_lo, s, kMsSs);
+    }
     ms_publish();
   }
   __syncthreads();
-  // Q's images as they are, for the next kernel's bulk copies (rows past r16 are not read)
+  // Q's images as they are (rows past r16 are not read)
   uint4* dst = reinterpret_cast<uint4*>(a.q + static_cast<int64_t>(g) * 2 * kMsImage);
   for (int i = threadIdx.x; i < 2 * kMsImage / 16; i += kMsThreads)
     if ((i * 16 % kMsBlock) / 128 < a.r16) dst[i] = *reinterpret_cast<const uint4*>(q_hi + 16 * i);
   ms_end(tmem, 256);
 }
 
-// Grid (parts, groups).  X of a piece: Q times it (or it times Q), in fp32 through shared
-// memory to rows of 512 bytes, so that weights and results move whole row segments.
+// X of a run of units: Q times the piece (or the piece times Q), in fp32 through shared memory
+// to rows of 512 bytes, so that weights and results move whole row segments.  The next
+// piece's loads run beside the product and the stores.
 template <typename T, bool VEC, bool OUT_VEC>
-__global__ void __launch_bounds__(kMsThreads) muon_apply_kernel(const __grid_constant__ MuonSmallArgs a) {
+__global__ void __launch_bounds__(kMsThreads, 1) muon_apply_kernel(const __grid_constant__ MuonSmallArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* hi = ms_smem(smem_raw);
   uint8_t *lo = hi + kMsImage, *q_hi = hi + 2 * kMsImage;
@@ -454,19 +502,27 @@ __global__ void __launch_bounds__(kMsThreads) muon_apply_kernel(const __grid_con
   const uint32_t tmem = ms_begin(ctl, 128);
   pdl_wait();
   pdl_trigger();
-  const int warp = warp_id(), lane = lane_id(), g = blockIdx.y;
-  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 64;
-  const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(g) * 2 * kMsImage);
-  for (int i = threadIdx.x; i < 2 * kMsImage / 16; i += kMsThreads)
-    if ((i * 16 % kMsBlock) / 128 < a.r16) *reinterpret_cast<uint4*>(q_hi + 16 * i) = __ldg(src + i);
-  const double inv = a.inv_norm[g];
-  const int64_t base = static_cast<int64_t>(g) * a.rows * a.cols;
+  const int warp = warp_id(), lane = lane_id();
+  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 32;
+  const int64_t u0 = ms_first(a, blockIdx.x, gridDim.x), u1 = ms_first(a, blockIdx.x + 1, gridDim.x);
   uint32_t phase = 0;
-  bool ok = true;
-  for (int piece = blockIdx.x; piece < a.pieces && ok; piece += gridDim.x) {
-    float4 u[16];
-    ms_load<T, VEC, false>(a, g, piece, u);
-    const int e = ms_image(a, u, hi, lo, ctl->red);
+  MsRaw u;
+  int g = static_cast<int>(u0 / a.pieces), piece = static_cast<int>(u0 - static_cast<int64_t>(g) * a.pieces);
+  int g_q = -1;
+  double inv = 0.0;
+  if (u0 < u1) ms_load<T, VEC, false>(a, g, piece, u);
+  for (int64_t v = u0; v < u1; ++v) {
+    if (g != g_q) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(g) * 2 * kMsImage);
+      for (int i = threadIdx.x; i < 2 * kMsImage / 16; i += kMsThreads)
+        if ((i * 16 % kMsBlock) / 128 < a.r16) *reinterpret_cast<uint4*>(q_hi + 16 * i) = __ldg(src + i);
+      inv = a.inv_norm[g];
+      g_q = g;
+    }
+    ms_form<VEC, false>(a, g, piece, u);
+    const int e = ms_image(a, u.g, hi, lo, ctl->red);
+    const int g_next = piece + 1 == a.pieces ? g + 1 : g, p_next = piece + 1 == a.pieces ? 0 : piece + 1;
+    if (v + 1 < u1) ms_load<T, VEC, false>(a, g_next, p_next, u);
     ms_publish();
     if (threadIdx.x == 0) {
       const uint32_t h = smem_u32(hi), l = smem_u32(lo), qh = smem_u32(q_hi), ql = qh + kMsImage;
@@ -475,30 +531,27 @@ __global__ void __launch_bounds__(kMsThreads) muon_apply_kernel(const __grid_con
       mma_commit(&ctl->bar);
     }
     const float f = static_cast<float>(inv * ldexp(1.0, -e));
-    ok = ms_wait(ctl, phase, a.status);
-    if (!ok) break;
+    if (!ms_wait(ctl, phase, a.status)) break;
     const int r0 = a.tall ? piece * 128 : 0, n0 = a.tall ? 0 : piece * 128;
     const int rows = min(128, a.rows - r0), cols = min(128, a.cols - n0);
-    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
+    uint32_t d[32];
+    tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, d);
+    tmem_ld_wait();
+    if (row < rows && c0 < cols) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t v[32];
-      tmem_ld_32x32b_x32(taddr + 32 * h, v);
-      tmem_ld_wait();
-      if (row < rows && c0 + 32 * h < cols) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(hi + row * 512 + (((c0 + 32 * h) / 4 + i) ^ (row & 7)) * 16) =
-              make_float4(f * __uint_as_float(v[4 * i]), f * __uint_as_float(v[4 * i + 1]),
-                          f * __uint_as_float(v[4 * i + 2]), f * __uint_as_float(v[4 * i + 3]));
-      }
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(hi + row * 512 + ((c0 / 4 + i) ^ (row & 7)) * 16) =
+            make_float4(f * __uint_as_float(d[4 * i]), f * __uint_as_float(d[4 * i + 1]),
+                        f * __uint_as_float(d[4 * i + 2]), f * __uint_as_float(d[4 * i + 3]));
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    for (int i = warp; i < rows; i += kMsThreads / 32) {
-      const int col = 4 * lane;
-      if (col >= cols) continue;
+    const int64_t base = static_cast<int64_t>(g) * a.rows * a.cols;
+#pragma unroll
+    for (int k = 0; k < kMsSlots; ++k) {
+      const int i = warp + kMsWarps * k, col = 4 * lane;
+      if (i >= rows || col >= cols) break;
       const float4 x4 = *reinterpret_cast<const float4*>(hi + i * 512 + ((lane ^ (i & 7)) * 16));
       float x[4] = {x4.x, x4.y, x4.z, x4.w};
       const int64_t at = base + static_cast<int64_t>(r0 + i) * a.cols + n0 + col;
@@ -519,6 +572,8 @@ __global__ void __launch_bounds__(kMsThreads) muon_apply_kernel(const __grid_con
           }
       }
     }
+    g = g_next;
+    piece = p_next;
     __syncthreads();  // the image is written again
   }
   ms_end(tmem, 128);
