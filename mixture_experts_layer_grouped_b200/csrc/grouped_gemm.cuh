@@ -256,8 +256,9 @@ struct TileQueue {
 };
 
 // Producer of rank 0 (or of a single CTA): the next tile, or `units` at the end.
-template <bool PAIR>
-__device__ __forceinline__ int claim_tile(TileQueue& q, const GemmParams& p, int units,
+// (P: parameters with unit_counter and status.)
+template <bool PAIR, typename P>
+__device__ __forceinline__ int claim_tile(TileQueue& q, const P& p, int units,
                                           volatile int* abort, bool& ok) {
   if (!q.dynamic) {
     const int u = q.next_static;
@@ -282,8 +283,8 @@ __device__ __forceinline__ int claim_tile(TileQueue& q, const GemmParams& p, int
 // Any other role: the next tile, or `units` at the end (or on a time-out).
 // A warp calls it with all lanes (one release per warp), a thread alone with
 // warp_wide = false.
-template <bool PAIR>
-__device__ __forceinline__ int next_tile(TileQueue& q, const GemmParams& p, int units, int rank,
+template <bool PAIR, typename P>
+__device__ __forceinline__ int next_tile(TileQueue& q, const P& p, int units, int rank,
                                          bool warp_wide, volatile int* abort) {
   if (!q.dynamic) {
     const int u = q.next_static;

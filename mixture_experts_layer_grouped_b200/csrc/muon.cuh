@@ -26,6 +26,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "grouped_gemm.cuh"  // packed f32x2 arithmetic
 #include "wgrad.cuh"         // MN-major descriptors
@@ -46,6 +48,8 @@ struct MuonInArgs {
   int64_t n;                // rows * cols
   int cols, ld, chunk, chunks, nesterov;
   float beta, eps;
+  int32_t* counters;        // zeroed here, for the products that follow
+  int n_counters;
 };
 
 template <typename T>
@@ -71,6 +75,8 @@ __global__ void __launch_bounds__(256) muon_norm_kernel(const __grid_constant__ 
   pdl_wait();
   pdl_trigger();
   __shared__ double red[8];
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < a.n_counters; i += 256) a.counters[i] = 0;
   const int64_t base = static_cast<int64_t>(blockIdx.y) * a.n;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
   const int64_t i1 = min(i0 + a.chunk, a.n);
@@ -172,80 +178,131 @@ __global__ void __launch_bounds__(256) muon_scale_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// The three products of a step, one matrix of the stack after another.
+// The products of all steps, in one persistent kernel.
 // ---------------------------------------------------------------------------
-enum { kNsGram = 0, kNsPoly = 1, kNsApply = 2 };
+enum { kNsGram = 0, kNsPoly = 1, kNsApply = 2, kNsSum = 3 };
 
 constexpr int kNsBK = 64;
 constexpr int kNsOpBytes = 128 * kNsBK * 2;  // 16 KB an operand, stage and CTA
+constexpr int kNsStages = 4;
 constexpr int kNsEpiWarps = 8;
 constexpr int kNsThreads = 32 * (2 + kNsEpiWarps);
 constexpr int kNsBlkBytes = 32 * 32 * 2;     // an epilogue warp's block: 32 rows x 32 columns
+constexpr int kNsWarpBytes = 6 * kNsBlkBytes;  // the blocks it has in flight
+constexpr int kNsSets = 4;                   // at most, of one to three arrays each
+constexpr int kNsMaxSplits = 16;
+constexpr int kNsSmemBytes = kNsStages * 2 * kNsOpBytes + kNsEpiWarps * (kNsWarpBytes + 32 * 4) + 768 + 1024;
 
-// What a form of the kernel stages and how: its values are hi + lo (LO), it adds to the
-// product what a block brings (IN); the blocks an epilogue warp keeps in flight, and the
-// load stages in what they leave of shared memory.
-template <int MODE, bool PAIR, bool LAST>
-struct NsCfg {
-  static constexpr int TILE = PAIR ? 256 : 128;
-  static constexpr bool SPLIT = !PAIR;
-  static constexpr bool LO = MODE == kNsApply || SPLIT;
-  static constexpr bool IN = MODE != kNsGram;
-  static constexpr int ARR = (LO ? 2 : 1) + (LAST ? 1 : 0);  // arrays of a block
-  static constexpr int SETS = LAST ? 2 : (LO ? 3 : 4);
-  static constexpr int STAGES = LO ? 4 : 5;
-  static constexpr int STG = kNsEpiWarps * SETS * ARR * kNsBlkBytes;
-  static constexpr int SMEM_BYTES = STAGES * 2 * kNsOpBytes + STG + kNsEpiWarps * 32 * 4 + 512 + 1024;
-};
-
+// Work units in order: for each run of `chunk` matrices, for each step, the Gram tiles
+// (`splits` units each, and with more than one `sums` units that add them up), the
+// polynomial's tiles, the application's tiles.  Symmetric results: only tiles on and above
+// the diagonal.  CTAs (or pairs) claim units in this order, so what a
+// claimed unit waits for was claimed before by a running CTA, and every wait ends.
 struct NsParams {
-  // [groups, rows, K] K-major (box 64 x 128) or [groups, K, cols] (box 64 x 64)
-  CUtensorMap a, b;        // hi parts
-  CUtensorMap a_lo, b_lo;  // SPLIT: lo parts
-  CUtensorMap sym;         // not SPLIT poly and apply: the symmetric operand with box 64 x 64
+  // [groups, rows, K] K-major (box 64 x 128) or [groups, K, cols] (box 64 x 64); [buffer][hi, lo]
+  CUtensorMap x_gram[2][2], x_apply[2][2];
+  CUtensorMap ab_op[2][2];   // A and B [hi, lo]; lo only with SPLIT
+  CUtensorMap ab_mir[2];     // A and B with box 64 x 64, for the tiles below the diagonal
   // blocks of the epilogue (box 32 x 32, 64-byte swizzle)
-  CUtensorMap in_hi;       // poly: A; apply: X
-  CUtensorMap in_lo;       // apply; SPLIT poly
-  CUtensorMap out_hi;      // gram, poly: the symmetric result; apply: X'; last apply: out, if tma_out
-  CUtensorMap out_lo;      // apply; SPLIT gram and poly
-  CUtensorMap w_in;        // last apply: w, if tma_out
-  int32_t M, N, ksteps;    // output extents; 64-wide steps of the contraction
-  int32_t n_tiles, per_group, total;  // tiles
-  const float* in_diag;    // not SPLIT: [groups, r] remainders of A's (poly) or B's (apply) diagonal
-  float* out_diag;         // not SPLIT gram and poly
-  __nv_bfloat16* out;      // last apply: [groups, M, N]
-  const __nv_bfloat16* w;  // last apply: weights to update, or null (out = X)
-  int32_t tma_out;         // last apply: out and w have rows of whole 16-byte vectors
-  float alpha, beta;       // result = alpha * product + beta * in
-  float diag_scale;        // apply: in_diag times this is added to beta
-  float keep, step;        // weights: keep * w - step * X
+  CUtensorMap x_blk[2][2], ab_blk[2][2];
+  CUtensorMap out_map, w_map;  // last application, if tma_out
+  int32_t groups, rows, cols, r, steps, chunk;
+  int32_t sym_tiles, sym_n, app_tiles, app_n;  // tiles a matrix (n: tiles along a side, along columns)
+  int32_t k_gram, k_r;                         // 64-wide steps of the contractions
+  int32_t splits, sums;                        // sums: 0 with one split
+  int32_t total;
+  int32_t* unit_counter;       // [1]: claims
+  int32_t* done;               // [groups][3 * steps]: epilogue warps that finished a unit
+  int32_t* split_done;         // [groups][sym_tiles]: epilogue warps that left a partial tile
+  float4* partial;             // [groups][sym_tiles][splits][tile]
+  float* diag[2];              // [groups, r]: remainders of A's and B's diagonals (not SPLIT)
+  __nv_bfloat16* out;          // [groups, rows, cols]
+  const __nv_bfloat16* w;      // weights to update, or null (out = X)
+  int32_t tma_out;             // out and w have rows of whole 16-byte vectors
+  float a, b, c;
+  float keep, step;            // weights: keep * w - step * X
   int32_t* status;
 };
 
-struct NsTile {
-  int g, m0, n0;
+struct NsUnit {
+  int k, mode, g, tile, split, m0, n0;
 };
 
-// Symmetric results: only tiles on and above the diagonal are computed and stored.
-template <int MODE, int TILE>
-__device__ __forceinline__ NsTile ns_decode(const NsParams& p, int u) {
-  NsTile t;
-  t.g = u / p.per_group;
-  int v = u - t.g * p.per_group;
-  if (MODE == kNsApply) {
-    t.m0 = v / p.n_tiles;
-    t.n0 = (v - t.m0 * p.n_tiles) * TILE;
+template <int TILE>
+__device__ __forceinline__ NsUnit ns_decode(const NsParams& p, int u) {
+  NsUnit t;
+  const int per = p.sym_tiles * (p.splits + p.sums + 1) + p.app_tiles;  // units a matrix and step
+  const int64_t run = static_cast<int64_t>(p.chunk) * per * p.steps;
+  const int q = static_cast<int>(u / run);
+  int v = static_cast<int>(u - q * run);
+  const int first = q * p.chunk, n = min(p.chunk, p.groups - first);
+  t.k = v / (n * per);
+  v -= t.k * n * per;
+  t.split = 0;
+  if (v < n * p.sym_tiles * p.splits) {
+    t.mode = kNsGram;
+    t.g = v / (p.sym_tiles * p.splits);
+    v -= t.g * p.sym_tiles * p.splits;
+    t.tile = v / p.splits;
+    t.split = v - t.tile * p.splits;
+  } else if ((v -= n * p.sym_tiles * p.splits) < n * p.sym_tiles * p.sums) {
+    t.mode = kNsSum;  // split: the block column of the tile that it adds up
+    t.g = v / (p.sym_tiles * p.sums);
+    v -= t.g * p.sym_tiles * p.sums;
+    t.tile = v / p.sums;
+    t.split = v - t.tile * p.sums;
+  } else if ((v -= n * p.sym_tiles * p.sums) < n * p.sym_tiles) {
+    t.mode = kNsPoly;
+    t.g = v / p.sym_tiles;
+    t.tile = v - t.g * p.sym_tiles;
+  } else {
+    v -= n * p.sym_tiles;
+    t.mode = kNsApply;
+    t.g = v / p.app_tiles;
+    t.tile = v - t.g * p.app_tiles;
+  }
+  t.g += first;
+  if (t.mode == kNsApply) {
+    t.m0 = t.tile / p.app_n;
+    t.n0 = (t.tile - t.m0 * p.app_n) * TILE;
     t.m0 *= TILE;
   } else {
-    int i = 0;
-    while (v >= p.n_tiles - i) {
-      v -= p.n_tiles - i;
+    int i = 0, w = t.tile;
+    while (w >= p.sym_n - i) {
+      w -= p.sym_n - i;
       ++i;
     }
     t.m0 = i * TILE;
-    t.n0 = (i + v) * TILE;
+    t.n0 = (i + w) * TILE;
   }
   return t;
+}
+
+// 64-wide steps [k0, k1) of the contraction of a unit (of one pass).
+__device__ __forceinline__ void ns_ksteps(const NsParams& p, const NsUnit& t, int& k0, int& k1) {
+  k0 = 0;
+  k1 = p.k_r;
+  if (t.mode == kNsGram) {
+    k0 = p.k_gram * t.split / p.splits;
+    k1 = p.k_gram * (t.split + 1) / p.splits;
+  }
+}
+
+// What a unit reads is written: the product before it, of the same matrix, is complete.
+// (The applications before that one, too: each product waits for the one before.)
+template <int WARPS>
+__device__ __forceinline__ bool ns_ready(const NsParams& p, const NsUnit& t, volatile int* abort) {
+  if (t.mode == kNsSum)
+    return counter_wait(p.split_done + static_cast<int64_t>(t.g) * p.sym_tiles + t.tile,
+                        (t.k + 1) * p.splits * WARPS, abort, p.status);
+  const int phase = 3 * t.k + t.mode;
+  if (phase == 0) return true;
+  const int units = t.mode == kNsGram ? p.app_tiles
+                                      : p.sym_tiles * (t.mode == kNsPoly && p.sums > 0 ? p.sums : 1);
+  const bool ok = counter_wait(p.done + static_cast<int64_t>(t.g) * 3 * p.steps + phase - 1, units * WARPS,
+                               abort, p.status);
+  fence_proxy_async_global();
+  return ok;
 }
 
 // TMA store of a staged block; committed groups are waited for until their shared memory
@@ -274,66 +331,72 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// One of a step's products.  PAIR: clusters of two CTAs on 256 x 256 tiles (each CTA holds
-// 128 rows of A and of B), otherwise one CTA on 128 x 128 tiles, with the SPLIT products.
-// Persistent; two accumulators in TMEM, so that one tile's epilogue overlaps the next one's
-// products.  TALL: X stands on the left (rows > cols).
+// Adds one to a counter, after this thread's earlier writes (and those it knows of).
+__device__ __forceinline__ void counter_add(int32_t* p) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+}
+
+// PAIR: clusters of two CTAs on 256 x 256 tiles (each CTA holds 128 rows of A and of B),
+// otherwise one CTA on 128 x 128 tiles.  SPLIT: products of hi and lo parts (see the top).
+// Two accumulators in TMEM, so that one unit's epilogue overlaps the next one's products.
+// TALL: X stands on the left.
+//
+// One kernel for all steps: a launch each took 12 us at 5 x [333, 215] (set-up, cold
+// instructions, drain) for 2 us of products; and a matrix goes on as soon as its own tiles
+// are done, not when the slowest of the stack are.
 //
 // A symmetric operand (A, B of the formulas) has only its tiles on and above the diagonal in
 // memory.  A k-step that needs rows of a tile below it loads the mirrored tile's rows and
 // hands them to the tensor cores MN-major: nothing is ever transposed in software.
 //
-// Epilogue: blocks of 32 x 32.  A TMA load brings what a block adds to the product two blocks
-// ahead, each lane works on one row of it in place, and a TMA store takes the result away
-// while the next blocks are worked on; loads and stores clip at the matrix's edges.  (Plain
+// Few tiles and a long contraction (one wide matrix): a Gram tile is `splits` units that leave
+// their fp32 sums in memory, and a unit for each block column adds them in order.
+//
+// Epilogue: blocks of 32 x 32.  A TMA load brings what a block adds to the product, ahead of
+// it, each lane works on one row of it in place, and a TMA store takes the result away: with
+// the others where the warp's blocks of a tile fit its buffers, otherwise while the next
+// blocks are worked on.  Loads and stores clip at the matrix's edges.  (Plain
 // loads and stores, one row a lane: 18 us a 256 x 256 tile, of which the products need 4.3.)
-template <int MODE, bool TALL, bool PAIR, bool LAST>
-__global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_constant__ NsParams p) {
-  using C = NsCfg<MODE, PAIR, LAST>;
-  constexpr int TILE = C::TILE;
-  constexpr bool SPLIT = C::SPLIT, LO = C::LO, IN = C::IN;
-  constexpr bool A_MN = MODE == kNsGram && TALL;
-  constexpr bool B_MN = (MODE == kNsGram && TALL) || (MODE == kNsApply && !TALL);
-  constexpr bool A_SYM = !SPLIT && (MODE == kNsPoly || (MODE == kNsApply && !TALL));
-  constexpr bool B_SYM = !SPLIT && (MODE == kNsPoly || (MODE == kNsApply && TALL));
-  constexpr bool COL_DIAG = !SPLIT && (MODE == kNsPoly || (MODE == kNsApply && TALL));
-  constexpr bool ROW_DIAG = !SPLIT && (MODE == kNsPoly || (MODE == kNsApply && !TALL));
-  const int steps = (SPLIT ? 3 : 1) * p.ksteps;  // hi hi, then hi lo and lo hi
+template <bool TALL, bool PAIR, bool SPLIT>
+__global__ void __launch_bounds__(kNsThreads, 1) ns_steps_kernel(const __grid_constant__ NsParams p) {
+  constexpr int TILE = PAIR ? 256 : 128;
+  constexpr int WARPS = PAIR ? 2 * kNsEpiWarps : kNsEpiWarps;  // epilogue warps of a unit
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* stg = ring + C::STAGES * 2 * kNsOpBytes;
-  float* dcols = reinterpret_cast<float*>(stg + C::STG);  // [kNsEpiWarps][32]
+  uint8_t* stg = ring + kNsStages * 2 * kNsOpBytes;
+  float* dcols = reinterpret_cast<float*>(stg + kNsEpiWarps * kNsWarpBytes);  // [kNsEpiWarps][32]
   uint64_t* full = reinterpret_cast<uint64_t*>(dcols + kNsEpiWarps * 32);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* acc_full = empty + C::STAGES;  // [2]
+  uint64_t* empty = full + kNsStages;
+  uint64_t* acc_full = empty + kNsStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;      // [2]
   uint64_t* drain = acc_empty + 2;
-  uint64_t* in_full = drain + 1;           // [kNsEpiWarps][SETS]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + kNsEpiWarps * C::SETS);
+  uint64_t* in_full = drain + 1;           // [kNsEpiWarps][kNsSets]
+  uint64_t* sched_full = in_full + kNsEpiWarps * kNsSets;  // [kSched]
+  uint64_t* sched_empty = sched_full + kSched;             // [kSched]
+  int* sched_u = reinterpret_cast<int*>(sched_empty + kSched);  // [kSched]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sched_u + kSched);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = warp_id(), lane = lane_id();
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
-  const int first = PAIR ? blockIdx.x / 2 : blockIdx.x;
-  const int step = PAIR ? gridDim.x / 2 : gridDim.x;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < kNsStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], PAIR ? 2 * kNsEpiWarps : kNsEpiWarps);
+      mbar_init(&acc_empty[b], WARPS);
     }
     mbar_init(drain, 1);
-    for (int i = 0; i < kNsEpiWarps * C::SETS; ++i) mbar_init(&in_full[i], 1);
+    for (int i = 0; i < kNsEpiWarps * kNsSets; ++i) mbar_init(&in_full[i], 1);
+    for (int i = 0; i < kSched; ++i) {
+      mbar_init(&sched_full[i], 1);
+      mbar_init(&sched_empty[i], PAIR ? 2 * (1 + kNsEpiWarps) : 1 + kNsEpiWarps);
+    }
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&p.a);
-    tma_prefetch_desc(&p.b);
-    tma_prefetch_desc(&p.out_hi);
-    if (IN) tma_prefetch_desc(&p.in_hi);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -350,6 +413,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
   pdl_trigger();
+  TileQueue tq{sched_full, sched_empty, sched_u, 0, 0u, 0, 0, true};
+  // (A or B) is a symmetric operand of a mode
+  auto a_sym = [](int mode) { return !SPLIT && (mode == kNsPoly || (mode == kNsApply && !TALL)); };
+  auto b_sym = [](int mode) { return !SPLIT && (mode == kNsPoly || (mode == kNsApply && TALL)); };
+  auto a_is_mn = [](int mode) { return mode == kNsGram && TALL; };
+  auto b_is_mn = [](int mode) { return (mode == kNsGram && TALL) || (mode == kNsApply && !TALL); };
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -357,38 +426,60 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
       const uint64_t pol = l2_policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t last[C::STAGES];
+      uint32_t last[kNsStages];
 #pragma unroll
-      for (int s = 0; s < C::STAGES; ++s) last[s] = 2;  // 2: nothing issued
+      for (int s = 0; s < kNsStages; ++s) last[s] = 2;  // 2: nothing issued
       bool ok = true;
-      for (int u = first; u < p.total && ok; u += step) {
-        const NsTile t = ns_decode<MODE, TILE>(p, u);
-        const int am = t.m0 + rank * 128, bn = t.n0 + rank * 128;
-        for (int kk = 0; kk < steps; ++kk) {
-          const int pass = SPLIT ? kk / p.ksteps : 0, k = (kk - pass * p.ksteps) * kNsBK;
-          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) { ok = false; break; }
-          uint8_t* sa = ring + stage * 2 * kNsOpBytes;
-          uint8_t* sb = sa + kNsOpBytes;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 4 : 2) * kNsOpBytes);
-          auto load = [&](uint8_t* dst, const CUtensorMap* map, bool mn, int row) {
+      while (ok) {
+        const int u = rank == 0 ? claim_tile<PAIR>(tq, p, p.total, abort_flag, ok)
+                                : next_tile<PAIR>(tq, p, p.total, rank, false, abort_flag);
+        if (u >= p.total) break;
+        const NsUnit t = ns_decode<TILE>(p, u);
+        if (t.mode == kNsSum) continue;
+        if (!ns_ready<WARPS>(p, t, abort_flag)) break;
+        const int am = t.m0 + rank * 128, bn = t.n0 + rank * 128, in = t.k & 1;
+        // operands [hi, lo]
+        const CUtensorMap* ma[2] = {&p.x_gram[in][0], &p.x_gram[in][1]};
+        const CUtensorMap* mb[2] = {ma[0], ma[1]};
+        const CUtensorMap* sym = &p.ab_mir[0];
+        if (t.mode != kNsGram) {
+          const int m = t.mode == kNsPoly ? 0 : 1;  // A, or B
+          sym = &p.ab_mir[m];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (!mn && j) break;
-              const int c0 = mn ? row + 64 * j : k, c1 = mn ? k : row;
-              if constexpr (PAIR)
-                tma_load_3d_pair(dst + 8192 * j, map, cluster_addr(&full[stage], 0), c0, c1, t.g, pol);
-              else
-                tma_load_3d(dst + 8192 * j, map, &full[stage], c0, c1, t.g, pol);
-            }
-          };
-          if (A_SYM && k < t.m0) load(sa, &p.sym, true, am);
-          else load(sa, pass == 2 ? &p.a_lo : &p.a, A_MN, am);
-          if (B_SYM && k < t.n0) load(sb, &p.sym, true, bn);
-          else load(sb, pass == 1 ? &p.b_lo : &p.b, B_MN, bn);
+          for (int j = 0; j < 2; ++j) {
+            ma[j] = mb[j] = &p.ab_op[m][j];
+            if (t.mode == kNsApply) (TALL ? ma : mb)[j] = &p.x_apply[in][j];
+          }
+        }
+        const bool amn = a_is_mn(t.mode), bmn = b_is_mn(t.mode), as = a_sym(t.mode), bs = b_sym(t.mode);
+        int k0, k1;
+        ns_ksteps(p, t, k0, k1);
+        for (int pass = 0; pass < (SPLIT ? 3 : 1) && ok; ++pass) {  // hi hi, then hi lo and lo hi
+          for (int kk = k0; kk < k1; ++kk) {
+            const int k = kk * kNsBK;
+            if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) { ok = false; break; }
+            uint8_t* sa = ring + stage * 2 * kNsOpBytes;
+            uint8_t* sb = sa + kNsOpBytes;
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 4 : 2) * kNsOpBytes);
+            auto load = [&](uint8_t* dst, const CUtensorMap* map, bool mn, int row) {
 #pragma unroll
-          for (int s = 0; s < C::STAGES; ++s)
-            if (s == stage) last[s] = phase;
-          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+              for (int j = 0; j < 2; ++j) {
+                if (!mn && j) break;
+                const int c0 = mn ? row + 64 * j : k, c1 = mn ? k : row;
+                if constexpr (PAIR)
+                  tma_load_3d_pair(dst + 8192 * j, map, cluster_addr(&full[stage], 0), c0, c1, t.g, pol);
+                else
+                  tma_load_3d(dst + 8192 * j, map, &full[stage], c0, c1, t.g, pol);
+              }
+            };
+            const bool at = as && k < t.m0, bt = bs && k < t.n0;  // below the diagonal
+            load(sa, at ? sym : ma[pass == 2], amn || at, am);
+            load(sb, bt ? sym : mb[pass == 1], bmn || bt, bn);
+#pragma unroll
+            for (int s = 0; s < kNsStages; ++s)
+              if (s == stage) last[s] = phase;
+            if (++stage == kNsStages) { stage = 0; phase ^= 1; }
+          }
         }
       }
       if (!PAIR) {
@@ -396,7 +487,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
         // issuer waits for every stage of either CTA, and the closing barrier for it
         const uint64_t t0 = global_timer_ns();
 #pragma unroll
-        for (int s = 0; s < C::STAGES; ++s) {
+        for (int s = 0; s < kNsStages; ++s) {
           if (last[s] > 1) continue;
           while (!mbar_try_wait(&full[s], last[s]) && global_timer_ns() - t0 < 20000000ull) {
           }
@@ -409,36 +500,45 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int u = first; u < p.total && ok; u += step) {
-        const NsTile t = ns_decode<MODE, TILE>(p, u);
+      while (ok) {
+        const int u = next_tile<PAIR>(tq, p, p.total, 0, false, abort_flag);
+        if (u >= p.total) break;
+        const NsUnit t = ns_decode<TILE>(p, u);
+        if (t.mode == kNsSum) continue;
         if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, p.status)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * TILE;
-        for (int k = 0; k < steps; ++k) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(ring + stage * 2 * kNsOpBytes);
-          const uint32_t sb = sa + kNsOpBytes;
-          const bool a_mn = A_MN || (A_SYM && k * kNsBK < t.m0);
-          const bool b_mn = B_MN || (B_SYM && k * kNsBK < t.n0);
-          const uint32_t idesc = idesc_f16(TILE, TILE, a_mn, b_mn);
-          // 16 of K on: 32 bytes inside the swizzle atom, or two groups of eight 128-byte rows
-          const uint64_t da = a_mn ? sdesc_mnmajor_sw128(sa, 8192) : sdesc_kmajor_sw128(sa);
-          const uint64_t db = b_mn ? sdesc_mnmajor_sw128(sb, 8192) : sdesc_kmajor_sw128(sb);
-          const uint32_t ka = a_mn ? 2048 >> 4 : 2, kb = b_mn ? 2048 >> 4 : 2;
+        const bool amn = a_is_mn(t.mode), bmn = b_is_mn(t.mode), as = a_sym(t.mode), bs = b_sym(t.mode);
+        int k0, k1;
+        ns_ksteps(p, t, k0, k1);
+        uint32_t accum = 0u;
+        for (int pass = 0; pass < (SPLIT ? 3 : 1) && ok; ++pass) {
+          for (int k = k0; k < k1; ++k) {
+            if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(ring + stage * 2 * kNsOpBytes);
+            const uint32_t sb = sa + kNsOpBytes;
+            const bool a_mn = amn || (as && k * kNsBK < t.m0);
+            const bool b_mn = bmn || (bs && k * kNsBK < t.n0);
+            const uint32_t idesc = idesc_f16(TILE, TILE, a_mn, b_mn);
+            // 16 of K on: 32 bytes inside the swizzle atom, or two groups of eight 128-byte rows
+            const uint64_t da = a_mn ? sdesc_mnmajor_sw128(sa, 8192) : sdesc_kmajor_sw128(sa);
+            const uint64_t db = b_mn ? sdesc_mnmajor_sw128(sb, 8192) : sdesc_kmajor_sw128(sb);
+            const uint32_t ka = a_mn ? 2048 >> 4 : 2, kb = b_mn ? 2048 >> 4 : 2;
 #pragma unroll
-          for (int kk = 0; kk < kNsBK / 16; ++kk) {
-            const uint32_t accum = (k | kk) != 0 ? 1u : 0u;
-            if constexpr (PAIR) mma_bf16_pair(d, da + kk * ka, db + kk * kb, idesc, accum);
-            else mma_bf16(d, da + kk * ka, db + kk * kb, idesc, accum);
+            for (int kk = 0; kk < kNsBK / 16; ++kk) {
+              if constexpr (PAIR) mma_bf16_pair(d, da + kk * ka, db + kk * kb, idesc, accum);
+              else mma_bf16(d, da + kk * ka, db + kk * kb, idesc, accum);
+              accum = 1u;
+            }
+            if constexpr (PAIR) {
+              mma_commit_pair(cluster_addr(&empty[stage], 0));
+              mma_commit_pair(cluster_addr(&empty[stage], 1));
+            } else {
+              mma_commit(&empty[stage]);
+            }
+            if (++stage == kNsStages) { stage = 0; phase ^= 1; }
           }
-          if constexpr (PAIR) {
-            mma_commit_pair(cluster_addr(&empty[stage], 0));
-            mma_commit_pair(cluster_addr(&empty[stage], 1));
-          } else {
-            mma_commit(&empty[stage]);
-          }
-          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
         }
         if (!ok) break;
         if constexpr (PAIR) {
@@ -457,86 +557,176 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
   } else {
     // ---------------- epilogue ----------------
     constexpr int BLKS = TILE / 64;    // blocks a warp has of a tile
-    constexpr int AHEAD = C::SETS - 1;
     const int quarter = warp & 3;      // TMEM lanes 32 * quarter ..
     const int half = (warp - 2) >> 2;  // column half of the tile
-    uint8_t* buf0 = stg + (warp - 2) * C::SETS * C::ARR * kNsBlkBytes;
+    uint8_t* buf0 = stg + (warp - 2) * kNsWarpBytes;
     float* dcol = dcols + (warp - 2) * 32;
-    uint64_t* my_full = in_full + (warp - 2) * C::SETS;
-    const bool weights = LAST && p.w != nullptr;
+    uint64_t* my_full = in_full + (warp - 2) * kNsSets;
     const uint64_t pol = l2_policy_evict_last();
+    uint32_t in_phase = 0;             // a bit for each set
+    int acc = 0;
+    uint32_t acc_phase = 0;
     // 16-byte vector v of this lane's row of array b of a set (64-byte swizzle)
     auto vec = [&](uint8_t* set, int b, int v) -> uint4* {
       return reinterpret_cast<uint4*>(set + b * kNsBlkBytes + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4));
     };
-    // the blocks asked for: a cursor AHEAD blocks in front (lane 0's loads, every lane's count)
-    int lu = first, lc = 0, lset = 0, asked = 0, taken = 0;
-    auto load_next = [&]() {
-      if (lu >= p.total) return;
-      if (lane == 0) {
-        const NsTile t = ns_decode<MODE, TILE>(p, lu);
-        const int m = t.m0 + rank * 128 + quarter * 32, n = t.n0 + half * (TILE / 2) + lc * 32;
-        const bool w_too = weights && p.tma_out;
-        uint8_t* set = buf0 + lset * C::ARR * kNsBlkBytes;
-        uint64_t* bar = my_full + lset;
-        mbar_arrive_expect_tx(bar, (1 + (LO ? 1 : 0) + (w_too ? 1 : 0)) * kNsBlkBytes);
-        tma_load_3d(set, &p.in_hi, bar, n, m, t.g, pol);
-        if (LO) tma_load_3d(set + kNsBlkBytes, &p.in_lo, bar, n, m, t.g, pol);
-        if (w_too) tma_load_3d(set + 2 * kNsBlkBytes, &p.w_in, bar, n, m, t.g, pol);
+
+    // A unit's blocks; false: gave up.  MODE kNsSum is the Gram tile's epilogue on sums of parts.
+    auto work = [&](const NsUnit& t, auto mode_c, auto last_c) -> bool {
+      constexpr int MODE = decltype(mode_c)::value;
+      constexpr bool LAST = decltype(last_c)::value;
+      constexpr bool GRAM = MODE == kNsGram || MODE == kNsSum;
+      constexpr bool LO = MODE == kNsApply || SPLIT;  // values are hi + lo
+      constexpr bool IN = !GRAM;
+      constexpr int ARR = (LO ? 2 : 1) + (LAST ? 1 : 0);
+      constexpr int SETS = BLKS < 6 / ARR ? BLKS : 6 / ARR;
+      constexpr bool ALL = SETS == BLKS;              // every block has its own buffers
+      constexpr int AHEAD = ALL ? SETS : SETS - 1;
+      constexpr bool COL_DIAG = !SPLIT && (MODE == kNsPoly || (MODE == kNsApply && TALL));
+      constexpr bool ROW_DIAG = !SPLIT && (MODE == kNsPoly || (MODE == kNsApply && !TALL));
+      static_assert(SETS <= kNsSets, "blocks of a warp");
+      const int M = MODE == kNsApply ? p.rows : p.r, N = MODE == kNsApply ? p.cols : p.r;
+      const int in = t.k & 1;
+      const CUtensorMap *in_hi = nullptr, *in_lo = nullptr, *out_hi, *out_lo;
+      float alpha, beta = 0.f, diag_scale = 0.f;
+      if (GRAM) {
+        out_hi = &p.ab_blk[0][0];
+        out_lo = &p.ab_blk[0][1];
+        alpha = kNsSa / (kNsSx * kNsSx);
+      } else if (MODE == kNsPoly) {
+        in_hi = &p.ab_blk[0][0];
+        in_lo = &p.ab_blk[0][1];
+        out_hi = &p.ab_blk[1][0];
+        out_lo = &p.ab_blk[1][1];
+        alpha = p.c * (kNsSb / (kNsSa * kNsSa));
+        beta = p.b * (kNsSb / kNsSa);
+        diag_scale = alpha;
+      } else {
+        constexpr float f = LAST ? 1.f / kNsSx : 1.f;  // the last one is X itself
+        in_hi = &p.x_blk[in][0];
+        in_lo = &p.x_blk[in][1];
+        out_hi = LAST ? &p.out_map : &p.x_blk[in ^ 1][0];
+        out_lo = &p.x_blk[in ^ 1][1];
+        alpha = f / kNsSb;
+        beta = p.a * f;
+        diag_scale = alpha;
       }
-      ++asked;
-      if (++lset == C::SETS) lset = 0;
-      if (++lc == BLKS) { lc = 0; lu += step; }
-    };
-    if (IN)
-      for (int i = 0; i < AHEAD; ++i) load_next();
-    int acc = 0, set_i = 0;
-    uint32_t acc_phase = 0, in_phase = 0;
-    bool ok = true;
-    const uint64_t alpha2 = f32x2_pack(p.alpha, p.alpha);
-    for (int u = first; u < p.total && ok; u += step) {
-      const NsTile t = ns_decode<MODE, TILE>(p, u);
+      const bool weights = LAST && p.w != nullptr, tma_out = !LAST || p.tma_out;
       const int mw = t.m0 + rank * 128 + quarter * 32, m = mw + lane;
-      const float* cd = p.in_diag + static_cast<int64_t>(t.g) * (COL_DIAG ? p.N : p.M);
-      const float dm = ROW_DIAG && m < p.M ? __ldg(cd + m) : 0.f;
-      const float f_row = fmaf(p.diag_scale, dm, p.beta);
-      // (a lane that gave up takes its warp along)
-      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase, abort_flag, p.status))) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < BLKS; ++c) {
-        const int n = t.n0 + half * (TILE / 2) + c * 32;
-        uint8_t* set = buf0 + set_i * C::ARR * kNsBlkBytes;
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * TILE +
-                               half * (TILE / 2) + c * 32, r);
-        if (COL_DIAG) dcol[lane] = n + lane < p.N ? __ldg(cd + n + lane) : 0.f;
-        if (IN) {
-          ok = __all_sync(0xffffffffu, mbar_wait(my_full + set_i, in_phase, abort_flag, p.status));
-          if (ok) ++taken;
+      const int nw = t.n0 + half * (TILE / 2);
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * TILE +
+                             half * (TILE / 2);
+      int asked = 0, taken = 0;
+      auto load_next = [&]() {  // lane 0
+        const int c = asked++, set_i = c % SETS;
+        uint8_t* set = buf0 + set_i * ARR * kNsBlkBytes;
+        uint64_t* bar = my_full + set_i;
+        mbar_arrive_expect_tx(bar, ((LO ? 2 : 1) + (weights && tma_out ? 1 : 0)) * kNsBlkBytes);
+        tma_load_3d(set, in_hi, bar, nw + 32 * c, mw, t.g, pol);
+        if (LO) tma_load_3d(set + kNsBlkBytes, in_lo, bar, nw + 32 * c, mw, t.g, pol);
+        if (weights && tma_out) tma_load_3d(set + 2 * kNsBlkBytes, &p.w_map, bar, nw + 32 * c, mw, t.g, pol);
+      };
+      auto store = [&](int c) {  // lane 0
+        uint8_t* set = buf0 + (c % SETS) * ARR * kNsBlkBytes;
+        if (mw < M && nw + 32 * c < N && tma_out) {
+          tma_store_3d(out_hi, set, nw + 32 * c, mw, t.g);
+          if (LO && !LAST) tma_store_3d(out_lo, set + kNsBlkBytes, nw + 32 * c, mw, t.g);
         }
-        tmem_ld_wait();
-        if (!ok) break;
-        if (c == BLKS - 1) {  // the accumulator is in registers: hand it back
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (PAIR) mbar_arrive_cluster(cluster_addr(&acc_empty[acc], 0));
-            else mbar_arrive(&acc_empty[acc]);
-          }
-        } else if (COL_DIAG) {
-          __syncwarp();
-        }
-        const bool some = mw < p.M && n < p.N;
-        const bool on_diag = MODE != kNsApply && mw == n;
-        if (some) {
+      };
+      bool ok = true;
+      if (IN || MODE == kNsSum) {
+        if (lane == 0) ok = ns_ready<WARPS>(p, t, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        __syncwarp();  // what lane 0 has seen, the warp has
+        if (IN && ok && lane == 0)
+          for (int i = 0; i < AHEAD; ++i) load_next();
+      }
+      // A's or B's diagonal remainders (rewritten every step: no ldg)
+      const float* cd = p.diag[MODE == kNsPoly ? 0 : 1] + static_cast<int64_t>(t.g) * p.r;
+      const float dm = ROW_DIAG && ok && m < M ? __ldcg(cd + m) : 0.f;
+      float dn[BLKS];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {  // eight columns
+      for (int c = 0; c < BLKS; ++c)
+        dn[c] = COL_DIAG && ok && nw + 32 * c + lane < N ? __ldcg(cd + nw + 32 * c + lane) : 0.f;
+      const float f_row = fmaf(diag_scale, dm, beta);
+      // (a lane that gave up takes its warp along)
+      if (MODE != kNsSum) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase, abort_flag, p.status));
+        tc_fence_after();
+      }
+      const uint64_t alpha2 = f32x2_pack(alpha, alpha);
+      const int c_first = MODE == kNsSum ? t.split : 0, c_end = MODE == kNsSum ? t.split + 1 : BLKS;
+#pragma unroll 1
+      for (int c = c_first; c < c_end && ok; ++c) {
+        const int n = nw + c * 32, set_i = c % SETS;
+        uint8_t* set = buf0 + set_i * ARR * kNsBlkBytes;
+        const bool some = mw < M && n < N;
+        uint32_t wv[LAST ? 16 : 1];  // weights of any alignment: one column a lane, two rows a word
+        if (LAST && weights && !tma_out && some && n + lane < N) {
+          const int64_t o = (static_cast<int64_t>(t.g) * M + mw) * N + n + lane;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint32_t w0 = mw + i < M ? __bfloat16_as_ushort(p.w[o + static_cast<int64_t>(i) * N]) : 0u;
+            const uint32_t w1 = mw + i + 1 < M ? __bfloat16_as_ushort(p.w[o + static_cast<int64_t>(i + 1) * N]) : 0u;
+            wv[LAST ? i / 2 : 0] = w0 | (w1 << 16);
+          }
+        }
+        if (COL_DIAG) {
+          float d = dn[0];
+#pragma unroll
+          for (int i = 1; i < BLKS; ++i)
+            if (c == i) d = dn[i];
+          dcol[lane] = d;
+        }
+        if (IN) {
+          ok = __all_sync(0xffffffffu, mbar_wait(my_full + set_i, (in_phase >> set_i) & 1, abort_flag, p.status));
+          if (!ok) break;
+          in_phase ^= 1u << set_i;
+          ++taken;
+        }
+        __syncwarp();
+        const bool on_diag = MODE != kNsApply && mw == n;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {  // 16 columns
+          uint32_t r[16];
+          if constexpr (MODE == kNsSum) {
+            // parts as the other CTAs' same warps and lanes left them: [split][block][h][4][lane]
+            const float4* part = p.partial +
+                (static_cast<int64_t>(t.g) * p.sym_tiles + t.tile) * p.splits * (TILE * TILE / 4) +
+                (rank * kNsEpiWarps + warp - 2) * (BLKS * 256) + (2 * c + h) * 128 + lane;
+            float4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int s = 0; s < p.splits; ++s)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 x = __ldcg(part + static_cast<int64_t>(s) * (TILE * TILE / 4) + 32 * i);
+                v[i].x += x.x;
+                v[i].y += x.y;
+                v[i].z += x.z;
+                v[i].w += x.w;
+              }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              r[4 * i] = __float_as_uint(v[i].x);
+              r[4 * i + 1] = __float_as_uint(v[i].y);
+              r[4 * i + 2] = __float_as_uint(v[i].z);
+              r[4 * i + 3] = __float_as_uint(v[i].w);
+            }
+          } else {
+            tmem_ld_32x32b_x16(taddr + 32 * c + 16 * h, r);
+            tmem_ld_wait();
+          }
+          if (!some) continue;
+#pragma unroll
+          for (int qq = 0; qq < 2; ++qq) {  // eight columns
+            const int q = 2 * h + qq;
             uint64_t v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              v[i] = f32x2_mul(alpha2, f32x2_pack(__uint_as_float(r[8 * q + 2 * i]),
-                                                  __uint_as_float(r[8 * q + 2 * i + 1])));
+              v[i] = f32x2_mul(alpha2, f32x2_pack(__uint_as_float(r[8 * qq + 2 * i]),
+                                                  __uint_as_float(r[8 * qq + 2 * i + 1])));
             if (IN) {
               const uint4 h4 = *vec(set, 0, q);
               uint4 l4 = make_uint4(0, 0, 0, 0);
@@ -560,7 +750,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
                 // (A + D)^2 = A^2 + D A + A D
                 uint64_t f = f32x2_pack(f_row, f_row);
                 if (COL_DIAG)
-                  f = f32x2_fma(f32x2_pack(p.diag_scale, p.diag_scale), f32x2_pack(d[2 * i], d[2 * i + 1]), f);
+                  f = f32x2_fma(f32x2_pack(diag_scale, diag_scale), f32x2_pack(d[2 * i], d[2 * i + 1]), f);
                 v[i] = f32x2_fma(f, x, v[i]);
               }
             }
@@ -570,10 +760,10 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
             if (MODE == kNsPoly && !SPLIT && on_diag && (lane >> 3) == q) {  // b D
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if ((lane & 7) == i) y[i] = fmaf(p.beta, dm, y[i]);
+                if ((lane & 7) == i) y[i] = fmaf(beta, dm, y[i]);
             }
             if constexpr (LAST) {
-              if (weights && p.tma_out) {
+              if (weights && tma_out) {
                 const uint4 w4 = *vec(set, 2, q);
                 const __nv_bfloat162* w2 = reinterpret_cast<const __nv_bfloat162*>(&w4);
 #pragma unroll
@@ -583,7 +773,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
                   y[2 * i + 1] = fmaf(p.keep, wf.y, -p.step * y[2 * i + 1]);
                 }
               }
-              if (p.tma_out) {
+              if (tma_out) {
                 *vec(set, 0, q) = make_uint4(bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3]),
                                              bf16x2_bits(y[4], y[5]), bf16x2_bits(y[6], y[7]));
               } else {  // fp32 over the lane's own hi and lo vectors, written out below
@@ -604,55 +794,132 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
               }
               *vec(set, 0, q) = h4;
               if (LO) *vec(set, 1, q) = l4;
-              if (MODE != kNsApply && !SPLIT && on_diag && (lane >> 3) == q && m < p.M) {
+              if (MODE != kNsApply && !SPLIT && on_diag && (lane >> 3) == q && m < M) {
                 const __half* hh = reinterpret_cast<const __half*>(&h4);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                   if ((lane & 7) == i)
-                    p.out_diag[static_cast<int64_t>(t.g) * p.M + m] = y[i] - __half2float(hh[i]);
+                    p.diag[MODE == kNsPoly ? 1 : 0][static_cast<int64_t>(t.g) * p.r + m] =
+                        y[i] - __half2float(hh[i]);
               }
             }
           }
         }
-        if (LAST && !p.tma_out && some) {
-          // rows of any alignment: one column a lane, one row after another
+        if (MODE != kNsSum && c == BLKS - 1) {  // the accumulator is read: hand it back
+          tc_fence_before();
           __syncwarp();
-          if (n + lane < p.N) {
+          if (lane == 0) {
+            if (PAIR) mbar_arrive_cluster(cluster_addr(&acc_empty[acc], 0));
+            else mbar_arrive(&acc_empty[acc]);
+          }
+        }
+        if (LAST && !tma_out && some) {
+          __syncwarp();
+          if (n + lane < N) {
             const int b = (lane >> 2) & 1, v8 = lane >> 3;
-            for (int i = 0; i < 32 && mw + i < p.M; ++i) {
-              const int64_t o = (static_cast<int64_t>(t.g) * p.M + mw + i) * p.N + n + lane;
+            const int64_t o = (static_cast<int64_t>(t.g) * M + mw) * N + n + lane;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
               float x = *reinterpret_cast<const float*>(set + b * kNsBlkBytes + i * 64 +
                                                         ((v8 ^ ((i >> 1) & 3)) << 4) + (lane & 3) * 4);
-              if (weights) x = fmaf(p.keep, __bfloat162float(p.w[o]), -p.step * x);
-              p.out[o] = __float2bfloat16_rn(x);
+              if (weights)
+                x = fmaf(p.keep, __uint_as_float(i & 1 ? wv[LAST ? i / 2 : 0] & 0xFFFF0000u : wv[LAST ? i / 2 : 0] << 16),
+                         -p.step * x);
+              if (mw + i < M) p.out[o + static_cast<int64_t>(i) * N] = __float2bfloat16_rn(x);
             }
           }
         }
+        if (!ALL) {
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            store(c);
+            bulk_commit();
+            bulk_wait_read<1>();  // the store before: the set that the next load uses
+            if (asked < BLKS) load_next();
+          }
+        }
+        __syncwarp();
+      }
+      if (ALL && ok) {
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-          if (some && !(LAST && !p.tma_out)) {
-            tma_store_3d(&p.out_hi, set, n, mw, t.g);
-            if (LO && !LAST) tma_store_3d(&p.out_lo, set + kNsBlkBytes, n, mw, t.g);
-          }
+          for (int c = c_first; c < c_end; ++c) store(c);
           bulk_commit();
-          // the set that the next load (IN) or the next block uses: its store is done reading
-          bulk_wait_read<IN ? 1 : C::SETS - 1>();
         }
-        if (IN) load_next();
+      }
+      if (IN && !ok && lane == 0) {
+        // gave up: the blocks asked for land before the CTA may leave (20 ms at most)
+        const uint64_t t0 = global_timer_ns();
+        for (; taken < asked; ++taken) {
+          const int set_i = taken % SETS;
+          while (!mbar_try_wait(my_full + set_i, (in_phase >> set_i) & 1) &&
+                 global_timer_ns() - t0 < 20000000ull) {
+          }
+          in_phase ^= 1u << set_i;
+        }
+      }
+      return ok;
+    };
+
+    // A part of a Gram tile: the accumulator as it is, [block][h][4][lane] of float4 a warp.
+    auto leave_part = [&](const NsUnit& t) -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase, abort_flag, p.status))) return false;
+      tc_fence_after();
+      float4* part = p.partial +
+          ((static_cast<int64_t>(t.g) * p.sym_tiles + t.tile) * p.splits + t.split) * (TILE * TILE / 4) +
+          (rank * kNsEpiWarps + warp - 2) * (BLKS * 256) + lane;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * TILE +
+                             half * (TILE / 2);
+#pragma unroll 1
+      for (int c = 0; c < 2 * BLKS; ++c) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(taddr + 16 * c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          part[c * 128 + 32 * i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                               __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_cluster(cluster_addr(&acc_empty[acc], 0));
+        else mbar_arrive(&acc_empty[acc]);
+        __threadfence();
+        counter_add(p.split_done + static_cast<int64_t>(t.g) * p.sym_tiles + t.tile);
+      }
+      return true;
+    };
+
+    while (true) {
+      const int u = next_tile<PAIR>(tq, p, p.total, rank, true, abort_flag);
+      if (u >= p.total) break;
+      const NsUnit t = ns_decode<TILE>(p, u);
+      using std::integral_constant;
+      using No = integral_constant<bool, false>;
+      bool ok;
+      if (t.mode == kNsGram && p.sums > 0) {
+        ok = leave_part(t);
+      } else {
+        if (t.mode == kNsSum) ok = work(t, integral_constant<int, kNsSum>(), No());
+        else if (t.mode == kNsGram) ok = work(t, integral_constant<int, kNsGram>(), No());
+        else if (t.mode == kNsPoly) ok = work(t, integral_constant<int, kNsPoly>(), No());
+        else if (t.k + 1 < p.steps) ok = work(t, integral_constant<int, kNsApply>(), No());
+        else ok = work(t, integral_constant<int, kNsApply>(), integral_constant<bool, true>());
+        if (ok && lane == 0) {
+          // the stores are done, and seen before the count is (also by other CTAs' TMA loads)
+          bulk_wait_all();
+          fence_proxy_async_global();
+          __threadfence();
+          counter_add(p.done + static_cast<int64_t>(t.g) * 3 * p.steps + 3 * t.k +
+                      (t.mode == kNsSum ? static_cast<int>(kNsGram) : t.mode));
+        }
         __syncwarp();
-        if (++set_i == C::SETS) { set_i = 0; in_phase ^= 1; }
       }
       if (!ok) break;
-      if (++acc == 2) { acc = 0; acc_phase ^= 1; }
-    }
-    if (IN && lane == 0 && taken < asked) {
-      // gave up: the blocks asked for land before the CTA may leave (20 ms at most)
-      const uint64_t t0 = global_timer_ns();
-      for (; taken < asked; ++taken)
-        while (!mbar_try_wait(my_full + taken % C::SETS, (taken / C::SETS) & 1) &&
-               global_timer_ns() - t0 < 20000000ull) {
-        }
+      if (t.mode != kNsSum && ++acc == 2) { acc = 0; acc_phase ^= 1; }
     }
     if (lane == 0) bulk_wait_all();
   }

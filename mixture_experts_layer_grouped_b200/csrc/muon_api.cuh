@@ -6,8 +6,9 @@
 namespace {
 
 struct MuonLayout {
-  size_t status, part, x[2][2], a[2], b[2], da, db, total;  // [buffer][hi, lo], [hi, lo]
+  size_t status, counters, part, x[2][2], a[2], b[2], diag[2], partial, total;  // [buffer][hi, lo], [hi, lo]
   int r, ld, ldr, chunk, chunks;
+  int tile, sym_n, sym_tiles, app_n, app_tiles, k_gram, k_r, splits, sums, n_counters;
 };
 
 // What the steps can reach from singular values in [0, 1], interval by interval: with
@@ -51,7 +52,7 @@ MuonBounds muon_bounds(const moe_muon_config& cfg) {
   return r;
 }
 
-// One-CTA tiles and products of hi and lo parts for matrices of at most 128 rows or columns.
+// Products of hi and lo parts for matrices of at most 128 rows or columns.
 bool muon_split(const moe_muon_config& c) { return c.rows <= 128 || c.cols <= 128; }
 
 // The r x r form (muon_small.cuh) where one extent is at most 128 and Q stays small: its
@@ -101,20 +102,43 @@ MuonLayout muon_layout(const moe_muon_config& c) {
   if (chunk < 4096) chunk = 4096;
   L.chunk = static_cast<int>(chunk);
   L.chunks = static_cast<int>((n + chunk - 1) / chunk);
+  const bool split = muon_split(c);
+  // 256 x 256 tiles by CTA pairs where they fill the GPU, one-CTA 128 x 128 tiles otherwise
+  // (each is done sooner, and there are more of them)
+  auto tiles = [&](int v) { return (v + L.tile - 1) / L.tile; };
+  L.tile = 256;
+  if (split || G * tiles(c.rows) * tiles(c.cols) < 74) L.tile = 128;
+  L.sym_n = tiles(L.r);
+  L.sym_tiles = L.sym_n * (L.sym_n + 1) / 2;
+  L.app_n = tiles(c.cols);
+  L.app_tiles = tiles(c.rows) * L.app_n;
+  L.k_gram = ((c.rows <= c.cols ? c.cols : c.rows) + kNsBK - 1) / kNsBK;
+  L.k_r = (L.r + kNsBK - 1) / kNsBK;
+  // Gram tiles that leave most of the GPU idle are split along the contraction (at least
+  // four 64-wide steps a part); a unit for each 32 columns of a warp's half tile adds them up
+  const int64_t ctas = L.tile == 128 ? 148 : 74, gram = static_cast<int64_t>(c.groups) * L.sym_tiles;
+  int64_t parts = gram < ctas ? ctas / gram : 1;
+  if (parts > kNsMaxSplits) parts = kNsMaxSplits;
+  if (parts > L.k_gram / 4) parts = L.k_gram / 4;
+  L.splits = parts < 1 ? 1 : static_cast<int>(parts);
+  L.sums = L.splits > 1 ? L.tile / 64 : 0;
+  // claims; finished warps a matrix and product; left parts a Gram tile
+  L.n_counters = static_cast<int>(1 + G * 3 * c.steps + (L.splits > 1 ? G * L.sym_tiles : 0));
   const size_t xb = G * static_cast<size_t>(c.rows) * L.ld * 2;
   const size_t ab = G * static_cast<size_t>(L.r) * L.ldr * 2;
   size_t o = 0;
   L.status = o; o = align_up(o + 4);
+  L.counters = o; o = align_up(o + static_cast<size_t>(L.n_counters) * 4);
   L.part = o; o = align_up(o + G * L.chunks * 8);
   for (int i = 0; i < 2; ++i)
     for (int j = 0; j < 2; ++j) { L.x[i][j] = o; o = align_up(o + xb); }
-  const bool split = muon_split(c);
   for (int j = 0; j < 2; ++j) {
     L.a[j] = o; o = align_up(o + (j == 0 || split ? ab : 0));
     L.b[j] = o; o = align_up(o + (j == 0 || split ? ab : 0));
   }
-  L.da = o; o = align_up(o + G * L.r * 4);
-  L.db = o; o = align_up(o + G * L.r * 4);
+  for (int j = 0; j < 2; ++j) { L.diag[j] = o; o = align_up(o + G * L.r * 4); }
+  L.partial = o;
+  o = align_up(o + G * L.sym_tiles * (L.splits > 1 ? L.splits : 0) * static_cast<size_t>(L.tile) * L.tile * 4);
   L.total = o;
   return L;
 }
@@ -152,13 +176,16 @@ moe_status make_ns_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_
   return MOE_OK;
 }
 
-template <int MODE, bool TALL, bool PAIR, bool LAST>
+// Persistent CTAs (pairs: clusters of two), as many as the units or the GPU has.
+template <bool TALL, bool PAIR, bool SPLIT>
 moe_status launch_ns(const NsParams& p, cudaStream_t s) {
-  auto kern = ns_gemm_kernel<MODE, TALL, PAIR, LAST>;
-  constexpr int smem = NsCfg<MODE, PAIR, LAST>::SMEM_BYTES;
-  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  auto kern = ns_steps_kernel<TALL, PAIR, SPLIT>;
+  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmemBytes));
   int ctas = sm_count() / (PAIR ? 2 : 1);
-  if (p.total < ctas) ctas = p.total;
+  // no more than one product of the whole stack keeps busy: a CTA that meets every product
+  // has its instructions at hand (5 x [333, 215]: 199 us with 74 pairs, XXX with 10)
+  const int64_t most = static_cast<int64_t>(p.groups) * std::max(p.sym_tiles * p.splits, p.app_tiles);
+  if (most < ctas) ctas = static_cast<int>(most);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   int n = 0;
@@ -176,7 +203,7 @@ moe_status launch_ns(const NsParams& p, cudaStream_t s) {
   }
   cfg.gridDim = dim3(PAIR ? 2 * ctas : ctas);
   cfg.blockDim = dim3(kNsThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kNsSmemBytes;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = n;
@@ -196,120 +223,70 @@ struct MuonArgs {
   float keep, step;
 };
 
-// The steps' three products on tiles of one CTA or of a pair.
-template <bool PAIR>
+// All steps' products on tiles of one CTA or of a pair.
+template <bool PAIR, bool SPLIT>
 moe_status ns_steps(const moe_muon_config& c, const MuonArgs& u, const MuonLayout& L, uint8_t* b,
                     cudaStream_t s) {
-  constexpr int TILE = PAIR ? 256 : 128;
   const bool wide = c.rows <= c.cols;
-  const int r = L.r;
-  const uint64_t G = c.groups, rows = c.rows, cols = c.cols;
-  auto float_at = [&](size_t off) { return reinterpret_cast<float*>(b + off); };
-  auto half_at = [&](size_t off) { return reinterpret_cast<__half*>(b + off); };
-  auto tiles = [](int n) { return (n + TILE - 1) / TILE; };
-  const int rt = tiles(r);
-  // maps of the working copies: X[buffer][hi, lo], A and B [hi, lo], as operands (a symmetric
-  // one also for its mirrored tiles) and as the epilogue's blocks
-  CUtensorMap x_gram[2][2], x_apply[2][2], x_block[2][2], ab_op[2][2], ab_block[2][2], ab_mirror[2];
+  const uint64_t G = c.groups, rows = c.rows, cols = c.cols, r = L.r;
+  NsParams p;
+  memset(&p, 0, sizeof(p));
   for (int j = 0; j < 2; ++j) {
     for (int i = 0; i < 2; ++i) {
       const void* x = b + L.x[i][j];
-      MOE_TRY(make_ns_map(&x_gram[i][j], x, cols, rows, G, L.ld, wide ? 128 : 64, 64));
-      MOE_TRY(make_ns_map(&x_apply[i][j], x, cols, rows, G, L.ld, wide ? 64 : 128, 64));
-      MOE_TRY(make_ns_map(&x_block[i][j], x, cols, rows, G, L.ld, 32, 32));
+      MOE_TRY(make_ns_map(&p.x_gram[i][j], x, cols, rows, G, L.ld, wide ? 128 : 64, 64));
+      MOE_TRY(make_ns_map(&p.x_apply[i][j], x, cols, rows, G, L.ld, wide ? 64 : 128, 64));
+      MOE_TRY(make_ns_map(&p.x_blk[i][j], x, cols, rows, G, L.ld, 32, 32));
       const void* ab = b + (i == 0 ? L.a[j] : L.b[j]);
-      if (PAIR && j) {  // A and B have no lo part there: not read
-        ab_op[i][j] = ab_op[i][0];
-        ab_block[i][j] = ab_block[i][0];
+      if (!SPLIT && j) {  // A and B have no lo part there: not read
+        p.ab_op[i][j] = p.ab_op[i][0];
+        p.ab_blk[i][j] = p.ab_blk[i][0];
         continue;
       }
-      MOE_TRY(make_ns_map(&ab_op[i][j], ab, r, r, G, L.ldr, 128, 64));
-      MOE_TRY(make_ns_map(&ab_block[i][j], ab, r, r, G, L.ldr, 32, 32));
-      if (j == 0) MOE_TRY(make_ns_map(&ab_mirror[i], ab, r, r, G, L.ldr, 64, 64));
+      MOE_TRY(make_ns_map(&p.ab_op[i][j], ab, r, r, G, L.ldr, 128, 64));
+      MOE_TRY(make_ns_map(&p.ab_blk[i][j], ab, r, r, G, L.ldr, 32, 32));
+      if (j == 0) MOE_TRY(make_ns_map(&p.ab_mir[i], ab, r, r, G, L.ldr, 64, 64));
     }
   }
-  NsParams sym;
-  memset(&sym, 0, sizeof(sym));
-  sym.M = sym.N = r;
-  sym.n_tiles = rt;
-  sym.per_group = rt * (rt + 1) / 2;
-  sym.total = c.groups * sym.per_group;
-  sym.status = status_ptr(b);
-  for (int k = 0; k < c.steps; ++k) {
-    const int in = k & 1;
-    // A = X X^T or X^T X
-    NsParams g = sym;
-    g.a = g.b = x_gram[in][0];
-    g.a_lo = g.b_lo = x_gram[in][1];
-    g.ksteps = ((wide ? c.cols : c.rows) + kNsBK - 1) / kNsBK;
-    g.in_hi = g.in_lo = g.w_in = g.sym = ab_block[0][0];  // not read
-    g.out_hi = ab_block[0][0];
-    g.out_lo = ab_block[0][1];
-    g.out_diag = float_at(L.da);
-    g.alpha = kNsSa / (kNsSx * kNsSx);
-    if (wide) MOE_TRY((launch_ns<kNsGram, false, PAIR, false>(g, s)));
-    else MOE_TRY((launch_ns<kNsGram, true, PAIR, false>(g, s)));
-    // B = b A + c A^2
-    NsParams q = sym;
-    q.a = q.b = ab_op[0][0];
-    q.a_lo = q.b_lo = ab_op[0][1];
-    q.ksteps = (r + kNsBK - 1) / kNsBK;
-    q.in_hi = q.w_in = ab_block[0][0];
-    q.in_lo = ab_block[0][1];
-    q.in_diag = float_at(L.da);
-    q.out_hi = ab_block[1][0];
-    q.out_lo = ab_block[1][1];
-    q.sym = ab_mirror[0];
-    q.out_diag = float_at(L.db);
-    q.alpha = c.c * kNsSb / (kNsSa * kNsSa);
-    q.beta = c.b * kNsSb / kNsSa;
-    q.diag_scale = q.alpha;
-    MOE_TRY((launch_ns<kNsPoly, false, PAIR, false>(q, s)));
-    // X' = a X + B X or a X + X B
-    NsParams x;
-    memset(&x, 0, sizeof(x));
-    x.M = c.rows;
-    x.N = c.cols;
-    x.n_tiles = tiles(c.cols);
-    x.per_group = tiles(c.rows) * x.n_tiles;
-    x.total = c.groups * x.per_group;
-    x.ksteps = q.ksteps;
-    x.a = wide ? ab_op[1][0] : x_apply[in][0];
-    x.a_lo = wide ? ab_op[1][1] : x_apply[in][1];
-    x.b = wide ? x_apply[in][0] : ab_op[1][0];
-    x.b_lo = wide ? x_apply[in][1] : ab_op[1][1];
-    x.in_hi = x_block[in][0];
-    x.in_lo = x_block[in][1];
-    x.out_hi = x_block[in ^ 1][0];
-    x.out_lo = x_block[in ^ 1][1];
-    x.w_in = x.in_hi;
-    x.sym = ab_mirror[1];
-    x.in_diag = float_at(L.db);
-    x.alpha = 1.f / kNsSb;
-    x.beta = c.a;
-    x.diag_scale = 1.f / kNsSb;
-    x.status = status_ptr(b);
-    if (k + 1 < c.steps) {
-      if (wide) MOE_TRY((launch_ns<kNsApply, false, PAIR, false>(x, s)));
-      else MOE_TRY((launch_ns<kNsApply, true, PAIR, false>(x, s)));
-      continue;
-    }
-    x.alpha /= kNsSx;  // X itself
-    x.beta /= kNsSx;
-    x.diag_scale /= kNsSx;
-    x.out = u.out;
-    x.w = u.w;
-    x.keep = u.keep;
-    x.step = u.step;
-    x.tma_out = c.cols % 8 == 0 && aligned16(u.out) && aligned16(u.w) ? 1 : 0;
-    if (x.tma_out) {
-      MOE_TRY(make_ns_map(&x.out_hi, u.out, cols, rows, G, cols, 32, 32));
-      if (u.w) MOE_TRY(make_ns_map(&x.w_in, u.w, cols, rows, G, cols, 32, 32));
-    }
-    if (wide) MOE_TRY((launch_ns<kNsApply, false, PAIR, true>(x, s)));
-    else MOE_TRY((launch_ns<kNsApply, true, PAIR, true>(x, s)));
+  p.tma_out = c.cols % 8 == 0 && aligned16(u.out) && aligned16(u.w) ? 1 : 0;
+  p.out_map = p.w_map = p.x_blk[0][0];  // not read without tma_out
+  if (p.tma_out) {
+    MOE_TRY(make_ns_map(&p.out_map, u.out, cols, rows, G, cols, 32, 32));
+    if (u.w) MOE_TRY(make_ns_map(&p.w_map, u.w, cols, rows, G, cols, 32, 32));
   }
-  return MOE_OK;
+  p.groups = c.groups;
+  p.rows = c.rows;
+  p.cols = c.cols;
+  p.r = L.r;
+  p.steps = c.steps;
+  p.chunk = c.groups;
+  p.sym_tiles = L.sym_tiles;
+  p.sym_n = L.sym_n;
+  p.app_tiles = L.app_tiles;
+  p.app_n = L.app_n;
+  p.k_gram = L.k_gram;
+  p.k_r = L.k_r;
+  p.splits = L.splits;
+  p.sums = L.sums;
+  const int64_t total = static_cast<int64_t>(c.groups) * c.steps *
+                        (static_cast<int64_t>(L.sym_tiles) * (L.splits + L.sums + 1) + L.app_tiles);
+  if (total > (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
+  p.total = static_cast<int32_t>(total);
+  int32_t* counters = reinterpret_cast<int32_t*>(b + L.counters);
+  p.unit_counter = counters;
+  p.done = counters + 1;
+  p.split_done = p.done + static_cast<size_t>(c.groups) * 3 * c.steps;
+  p.partial = reinterpret_cast<float4*>(b + L.partial);
+  for (int j = 0; j < 2; ++j) p.diag[j] = reinterpret_cast<float*>(b + L.diag[j]);
+  p.out = u.out;
+  p.w = u.w;
+  p.a = c.a;
+  p.b = c.b;
+  p.c = c.c;
+  p.keep = u.keep;
+  p.step = u.step;
+  p.status = status_ptr(b);
+  return wide ? launch_ns<false, PAIR, SPLIT>(p, s) : launch_ns<true, PAIR, SPLIT>(p, s);
 }
 
 template <typename K>
@@ -392,6 +369,8 @@ moe_status muon_run(const moe_muon_config& c, const MuonArgs& u, void* ws, cudaS
   a.nesterov = u.nesterov ? 1 : 0;
   a.beta = u.beta;
   a.eps = c.eps;
+  a.counters = reinterpret_cast<int32_t*>(b + L.counters);
+  a.n_counters = L.n_counters;
   // vectors of four where no vector crosses a row or a matrix's alignment
   const bool vec = c.cols % 4 == 0 && aligned16(u.grad) && aligned16(u.mom_in) && aligned16(u.mom_out);
   const dim3 grid(static_cast<unsigned>(L.chunks), static_cast<unsigned>(c.groups)), block(256);
@@ -407,7 +386,8 @@ moe_status muon_run(const moe_muon_config& c, const MuonArgs& u, void* ws, cudaS
   else
     MOE_TRY(vec ? in(muon_norm_kernel<float, true>, muon_scale_kernel<float, true>)
                 : in(muon_norm_kernel<float, false>, muon_scale_kernel<float, false>));
-  return muon_split(c) ? ns_steps<false>(c, u, L, b, s) : ns_steps<true>(c, u, L, b, s);
+  if (muon_split(c)) return ns_steps<false, true>(c, u, L, b, s);
+  return L.tile == 256 ? ns_steps<true, false>(c, u, L, b, s) : ns_steps<false, false>(c, u, L, b, s);
 }
 
 size_t muon_bytes(const moe_muon_config& c) {
