@@ -190,7 +190,7 @@ constexpr int kNsThreads = 32 * (2 + kNsEpiWarps);
 constexpr int kNsBlkBytes = 32 * 32 * 2;     // an epilogue warp's block: 32 rows x 32 columns
 constexpr int kNsWarpBytes = 6 * kNsBlkBytes;  // the blocks it has in flight
 constexpr int kNsSets = 4;                   // at most, of one to three arrays each
-constexpr int kNsMaxSplits = 16;
+constexpr int kNsMaxSplits = 8;
 constexpr int kNsSmemBytes = kNsStages * 2 * kNsOpBytes + kNsEpiWarps * (kNsWarpBytes + 32 * 4) + 768 + 1024;
 
 // Work units in order: for each run of `chunk` matrices, for each step, the Gram tiles
@@ -288,18 +288,38 @@ __device__ __forceinline__ void ns_ksteps(const NsParams& p, const NsUnit& t, in
   }
 }
 
+// counter_wait with short sleeps: a wait here is on the way of everything that follows.
+__device__ __forceinline__ bool ns_wait(const int32_t* p, int32_t target, volatile int* abort,
+                                        int32_t* status) {
+  uint64_t t0 = 0;
+  for (int i = 0;; ++i) {
+    int32_t v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    if (v >= target) return true;
+    if (*abort) return false;
+    if (i == 0) {
+      t0 = global_timer_ns();
+    } else if (global_timer_ns() - t0 > 2000000000ull) {
+      *abort = 1;
+      set_status(status, MOE_ERR_TIMEOUT);
+      return false;
+    }
+    __nanosleep(20);
+  }
+}
+
 // What a unit reads is written: the product before it, of the same matrix, is complete.
 // (The applications before that one, too: each product waits for the one before.)
 template <int WARPS>
 __device__ __forceinline__ bool ns_ready(const NsParams& p, const NsUnit& t, volatile int* abort) {
   if (t.mode == kNsSum)
-    return counter_wait(p.split_done + static_cast<int64_t>(t.g) * p.sym_tiles + t.tile,
+    return ns_wait(p.split_done + static_cast<int64_t>(t.g) * p.sym_tiles + t.tile,
                         (t.k + 1) * p.splits * WARPS, abort, p.status);
   const int phase = 3 * t.k + t.mode;
   if (phase == 0) return true;
   const int units = t.mode == kNsGram ? p.app_tiles
                                       : p.sym_tiles * (t.mode == kNsPoly && p.sums > 0 ? p.sums : 1);
-  const bool ok = counter_wait(p.done + static_cast<int64_t>(t.g) * 3 * p.steps + phase - 1, units * WARPS,
+  const bool ok = ns_wait(p.done + static_cast<int64_t>(t.g) * 3 * p.steps + phase - 1, units * WARPS,
                                abort, p.status);
   fence_proxy_async_global();
   return ok;
@@ -887,7 +907,6 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_steps_kernel(const __grid_co
       if (lane == 0) {
         if (PAIR) mbar_arrive_cluster(cluster_addr(&acc_empty[acc], 0));
         else mbar_arrive(&acc_empty[acc]);
-        __threadfence();
         counter_add(p.split_done + static_cast<int64_t>(t.g) * p.sym_tiles + t.tile);
       }
       return true;
@@ -912,7 +931,6 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_steps_kernel(const __grid_co
           // the stores are done, and seen before the count is (also by other CTAs' TMA loads)
           bulk_wait_all();
           fence_proxy_async_global();
-          __threadfence();
           counter_add(p.done + static_cast<int64_t>(t.g) * 3 * p.steps + 3 * t.k +
                       (t.mode == kNsSum ? static_cast<int>(kNsGram) : t.mode));
         }
