@@ -212,6 +212,19 @@ def _check(fn, code):
         raise MoEError(fn, code)
 
 
+_fns = {}
+
+
+def _call(fn, *args):
+    """A C function by name (looked up once), its status checked."""
+    f = _fns.get(fn)
+    if f is None:
+        f = _fns[fn] = getattr(lib(), fn)
+    code = f(*args)
+    if code != 0:
+        raise MoEError(fn, code)
+
+
 def moe_workspace_size(cfg: MoEConfig):
     b, r = ctypes.c_size_t(), ctypes.c_int32()
     _check("moe_workspace_size", lib().moe_workspace_size(ctypes.byref(cfg), ctypes.byref(b),
@@ -491,13 +504,13 @@ def moe_route_scored(cfg, router, topk_idx, topk_w, x=None, w_router=None, bias=
     """Routing by softmax or sigmoid scores: from x and w_router (with a workspace and
     logits_out), or from the logits alone (logits_in)."""
     bf, f32, T, E, k = torch.bfloat16, torch.float32, cfg.T, cfg.E, cfg.top_k
-    _check("moe_route_scored", lib().moe_route_scored(
-        cfg, router, _sized(x, bf, (T, cfg.H), "x"),
+    _call(
+        "moe_route_scored", cfg, router, _sized(x, bf, (T, cfg.H), "x"),
         _sized(w_router, bf, (E, cfg.H), "w_router"), _sized(bias, f32, (E,), "bias"),
         _sized(logits_in, f32, (T, E), "logits_in"),
         _sized(logits_out, f32, (T, E), "logits_out"),
         _sized(topk_idx, torch.int32, (T, k), "topk_idx"), _sized(topk_w, f32, (T, k), "topk_w"),
-        *_scratch(workspace), _stream(stream)))
+        *_scratch(workspace), _stream(stream))
 
 
 def _sequences(seq_offsets):
@@ -516,11 +529,11 @@ def moe_route_backward(cfg, router, logits, topk_idx, dgate, dlogits, dscore=Non
     same ``seq_offsets``) plus the balance loss's gradient, times the device scalar ``dloss``."""
     f32, T, E, k = torch.float32, cfg.T, cfg.E, cfg.top_k
     off, n_seq = _sequences(seq_offsets)
-    _check("moe_route_backward", lib().moe_route_backward(
-        cfg, router, _sized(logits, f32, (T, E), "logits"),
+    _call(
+        "moe_route_backward", cfg, router, _sized(logits, f32, (T, E), "logits"),
         _sized(topk_idx, torch.int32, (T, k), "topk_idx"), _sized(dgate, f32, (T, k), "dgate"),
         _sized(dscore, f32, (n_seq, E), "dscore"), off, n_seq, _sized(dloss, f32, (1,), "dloss"),
-        _sized(dlogits, f32, (T, E), "dlogits"), _stream(stream)))
+        _sized(dlogits, f32, (T, E), "dlogits"), _stream(stream))
 
 
 def moe_balance_workspace_size(cfg, n_seq=1) -> int:
@@ -535,11 +548,11 @@ def moe_balance_loss(cfg, router, logits, topk_idx, coef, loss, load, dscore, wo
     """Balance loss [1], load [n_seq, E] and dscore [n_seq, E] of the routed rows."""
     f32, i32, T, E = torch.float32, torch.int32, cfg.T, cfg.E
     off, n_seq = _sequences(seq_offsets)
-    _check("moe_balance_loss", lib().moe_balance_loss(
-        cfg, router, _sized(logits, f32, (T, E), "logits"),
+    _call(
+        "moe_balance_loss", cfg, router, _sized(logits, f32, (T, E), "logits"),
         _sized(topk_idx, i32, (T, cfg.top_k), "topk_idx"), off, n_seq, coef,
         _sized(loss, f32, (1,), "loss"), _sized(load, i32, (n_seq, E), "load"),
-        _sized(dscore, f32, (n_seq, E), "dscore"), *_scratch(workspace), _stream(stream)))
+        _sized(dscore, f32, (n_seq, E), "dscore"), *_scratch(workspace), _stream(stream))
 
 
 GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -566,9 +579,9 @@ def _grad(mcfg, t, name):
 
 def moe_orthogonalize(mcfg, g, out, workspace, stream=None):
     """out (bf16) = each matrix of g (fp32 or bf16) with its singular values moved to about 1."""
-    _check("moe_orthogonalize", lib().moe_orthogonalize(
-        mcfg, *_grad(mcfg, g, "g"), _stacked(mcfg, out, torch.bfloat16, "out"),
-        *_scratch(workspace), _stream(stream)))
+    _call(
+        "moe_orthogonalize", mcfg, *_grad(mcfg, g, "g"), _stacked(mcfg, out, torch.bfloat16, "out"),
+        *_scratch(workspace), _stream(stream))
 
 
 def moe_muon_step(mcfg, grad, momentum, momentum_out, w, w_out, workspace, beta=0.95,
@@ -576,11 +589,11 @@ def moe_muon_step(mcfg, grad, momentum, momentum_out, w, w_out, workspace, beta=
     """Momentum, orthogonalised update and weights of one optimiser step; ``momentum_out`` may
     be ``momentum`` and ``w_out`` may be ``w``."""
     f32, bf = torch.float32, torch.bfloat16
-    _check("moe_muon_step", lib().moe_muon_step(
-        mcfg, *_grad(mcfg, grad, "grad"), _stacked(mcfg, momentum, f32, "momentum"),
+    _call(
+        "moe_muon_step", mcfg, *_grad(mcfg, grad, "grad"), _stacked(mcfg, momentum, f32, "momentum"),
         _stacked(mcfg, momentum_out, f32, "momentum_out"), beta, 1 if nesterov else 0,
         _stacked(mcfg, w, bf, "w"), _stacked(mcfg, w_out, bf, "w_out"), step, decay,
-        *_scratch(workspace), _stream(stream)))
+        *_scratch(workspace), _stream(stream))
 
 
 class MoELayer:

@@ -19,6 +19,8 @@
 // is done again in 64 bits (measured at 256 experts, top 8 and a bias: under 1% of rows).
 #pragma once
 
+#include <cfloat>
+
 #include "common.cuh"
 
 namespace moe {
@@ -35,7 +37,7 @@ struct ScoredArgs {
   int32_t* topk_idx;      // [T, k]
   float* topk_w;          // [T, k]
   int T, E, G, g, k, size;  // size = E / G
-  int lanes_per_group;    // size / PER where that is a power of two and whole, otherwise 0
+  int lane_shift;         // log2(size / PER) where that is a whole power of two, otherwise -1
   int vec4;               // rows are whole 16-byte vectors
   uint32_t size_magic;    // ceil(2^32 / size): e / size == umulhi(e, magic) for e < 1024
   float rsf;
@@ -112,7 +114,7 @@ __device__ __forceinline__ K selected_share(bool soft, bool have, float l) {
 
 // Groups kept, as a bit mask, given the two largest keys that each of `lpg` lanes of a group
 // has seen (lane / lpg is the group).  margin (or null): distance of the last kept group's
-// score from the first one left out, less the roundings of their keys (+inf: none is left out).
+// score from the first one left out (+inf: none is left out).
 template <typename K>
 __device__ __forceinline__ uint32_t keep_of_tops(const ScoredArgs& a, int lane, K m1, K m2, int lpg,
                                                  float* margin) {
@@ -126,11 +128,7 @@ __device__ __forceinline__ uint32_t keep_of_tops(const ScoredArgs& a, int lane, 
     m2 = lo > s2 ? lo : s2;
   }
   K gs = m1;
-  float size = fabsf(float(m1));  // what the roundings of the score go by
-  if (a.group_top > 1 && m2 > K(-INFINITY)) {
-    gs += m2;
-    size += fabsf(float(m2));
-  }
+  if (a.group_top > 1 && m2 > K(-INFINITY)) gs += m2;
   gs = __shfl_sync(kAll, gs, (lane < a.G ? lane : 0) * lpg);
   if (lane >= a.G) gs = K(-INFINITY);
   int better = 0;
@@ -142,49 +140,67 @@ __device__ __forceinline__ uint32_t keep_of_tops(const ScoredArgs& a, int lane, 
   if (margin) {
     const uint32_t out = __reduce_max_sync(kAll, some && !kept ? ordered(float(gs)) : 0u);
     const uint32_t in = __reduce_min_sync(kAll, kept ? ordered(float(gs)) : 0xFFFFFFFFu);
-    const uint32_t most = __reduce_max_sync(kAll, m1 > K(-INFINITY) ? __float_as_uint(size) : 0u);
-    if (out != 0u) *margin = unordered(in) - unordered(out) - 2.4e-7f * __uint_as_float(most);
+    if (out != 0u) *margin = unordered(in) - unordered(out);
   }
   return __ballot_sync(kAll, kept);
 }
 
-// Whether the lane's own group is kept, where every group is `lpg` whole neighbouring lanes
-// (a power of two) and m1, m2 are the images of the lane's two largest keys (0: none).  The
-// lanes of a group share the comparisons with the other groups.
-__device__ __forceinline__ bool own_group_kept(const ScoredArgs& a, int lane, uint32_t m1, uint32_t m2,
-                                               int lpg, bool want_margin, float* margin) {
+// Whether the lane's own group is kept, where every group is 2^SHIFT whole neighbouring lanes
+// and m1, m2 are the lane's two largest keys.  The lanes of a group share the comparisons with
+// the other groups (by shuffles: rounds of warp-wide maxima took three times as long, their
+// reductions issue at a sixteenth of the rate).  margin: the last kept group's score less the
+// first one's left out.
+template <int SHIFT>
+__device__ __forceinline__ bool own_group_kept(const ScoredArgs& a, int lane, float m1, float m2,
+                                               bool want_margin, float* margin) {
   constexpr unsigned kAll = 0xffffffffu;
+  constexpr int lpg = 1 << SHIFT;
+#pragma unroll
   for (int o = 1; o < lpg; o <<= 1) {
-    const uint32_t o1 = __shfl_xor_sync(kAll, m1, o);
-    const uint32_t o2 = __shfl_xor_sync(kAll, m2, o);
-    m2 = max(min(m1, o1), max(m2, o2));
-    m1 = max(m1, o1);
+    const float o1 = __shfl_xor_sync(kAll, m1, o);
+    const float o2 = __shfl_xor_sync(kAll, m2, o);
+    m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+    m1 = fmaxf(m1, o1);
   }
-  const int q = lane / lpg, sub = lane - q * lpg;
-  const bool some = m1 != 0u && q < a.G;
-  float gs = -INFINITY, size = 0.f;
-  if (some) {
-    gs = unordered(m1);
-    size = fabsf(gs);
-    if (a.group_top > 1 && m2 != 0u) {
-      gs += unordered(m2);
-      size += fabsf(unordered(m2));
-    }
-  }
+  const int q = lane >> SHIFT;
+  float gs = m1;
+  if (a.group_top > 1 && m2 > -INFINITY) gs += m2;
+  if (q >= a.G) gs = -INFINITY;
   int better = 0;
-  for (int o = sub; o < ((a.G + lpg - 1) & ~(lpg - 1)); o += lpg) {
-    const float v = __shfl_sync(kAll, gs, (o < a.G ? o : 0) * lpg);
+#pragma unroll 2
+  for (int o0 = 0; o0 < a.G; o0 += lpg) {
+    const int o = o0 + (lane & (lpg - 1));
+    const float v = __shfl_sync(kAll, gs, (o << SHIFT) & 31);
     better += o < a.G && (v > gs || (v == gs && o < q)) ? 1 : 0;
   }
+#pragma unroll
   for (int o = 1; o < lpg; o <<= 1) better += __shfl_xor_sync(kAll, better, o);
-  const bool kept = some && better < a.g;
+  const bool some = gs > -INFINITY;
   if (want_margin) {
-    const uint32_t out = __reduce_max_sync(kAll, some && !kept ? ordered(gs) : 0u);
-    const uint32_t in = __reduce_min_sync(kAll, kept ? ordered(gs) : 0xFFFFFFFFu);
-    const uint32_t most = __reduce_max_sync(kAll, __float_as_uint(size));
-    if (out != 0u) *margin = unordered(in) - unordered(out) - 2.4e-7f * __uint_as_float(most);
+    const uint32_t first_out = __ballot_sync(kAll, some && better == a.g);
+    if (first_out != 0u) {  // then the places before it are taken
+      const uint32_t last_in = __ballot_sync(kAll, some && better == a.g - 1);
+      *margin = __shfl_sync(kAll, gs, __ffs(last_in) - 1) - __shfl_sync(kAll, gs, __ffs(first_out) - 1);
+    }
   }
-  return kept;
+  return some && better < a.g;
+}
+
+// The warp's 32 values in descending order (lane 0 the largest): a bitonic network whose
+// merges start mirrored, so that the lower lane of every exchange takes the larger value.
+__device__ __forceinline__ float warp_sort_desc(float v, int lane) {
+  const bool low[5] = {(lane & 1) == 0, (lane & 2) == 0, (lane & 4) == 0, (lane & 8) == 0, (lane & 16) == 0};
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    float o = __shfl_xor_sync(0xffffffffu, v, (2 << k) - 1);
+    v = low[k] ? fmaxf(v, o) : fminf(v, o);
+#pragma unroll
+    for (int j = k - 1; j >= 0; --j) {
+      o = __shfl_xor_sync(0xffffffffu, v, 1 << j);
+      v = low[j] ? fmaxf(v, o) : fminf(v, o);
+    }
+  }
+  return v;
 }
 
 // The same with the keys in shared memory: lpg lanes a group (one when G does not divide
@@ -318,14 +334,16 @@ constexpr int kRsCand = 64;  // candidates of a row
 // shared memory, one or two a lane, and each finds its rank by comparing itself to all.
 // That takes about half the instructions of k rounds of maximum and removal (and one round
 // more with a bias, whose next key the border check needs).
-template <int PER>
+// SOFT, BIASED: the form, 0 or 1, or -1 where it is asked for row by row.
+template <int PER, int SOFT, int BIASED>
 __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const float (&l)[PER],
-                                          const float (&bias)[PER], const float* row, float* sh) {
+                                          const float (&bias)[PER], float bias_max, const float* row,
+                                          float* sh) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  const bool biased = a.bias != nullptr;
-  const bool by_score = a.G > 1 && !biased && a.group_top > 1;
-  const bool soft = a.score == MOE_SCORE_SOFTMAX;
+  const bool biased = BIASED < 0 ? a.bias != nullptr : BIASED == 1;
+  const bool soft = SOFT < 0 ? a.score == MOE_SCORE_SOFTMAX : SOFT == 1;
+  const bool by_score = !biased && a.G > 1 && a.group_top > 1;
   // the softmax's maximum and sum, where a score of the whole row is asked for
   float lmax = -INFINITY, z = 1.f, smax = 1.f;
   if (soft && (biased || by_score || !a.renorm)) {
@@ -345,67 +363,70 @@ __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const floa
   // error of such a score, doubled, relative to the row's largest: the exponential's and the
   // division's roundings, and for a softmax the sum's (PER + 5 additions)
   const float eps = (soft ? 8e-6f : 1e-6f) * smax;
-  uint32_t key[PER];
-  if (biased) {
+  float key[PER];  // -inf: none (a bias that takes an expert out is -inf)
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const float v = key_score(l[i]) + bias[i];  // (a zero's sign is left to the border check)
-      key[i] = l[i] > -INFINITY && v > -INFINITY ? ordered_bits(v) : 0u;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = l[i] > -INFINITY ? ordered_bits(__fadd_rn(l[i], 0.f)) : 0u;
-  }
+  for (int i = 0; i < PER; ++i) key[i] = biased ? (l[i] > -INFINITY ? key_score(l[i]) + bias[i] : -INFINITY) : l[i];
+  float top = -INFINITY, second = -INFINITY;  // the lane's largest
+  bool kept = true;                           // its group is
   if (a.G > 1) {
     float margin = INFINITY;
-    const int per_group = a.lanes_per_group;
-    if (per_group > 0) {  // a group is so many whole lanes, a power of two
-      uint32_t m1 = 0u, m2 = 0u;
+    if (a.lane_shift >= 0) {  // a group is 2^lane_shift whole lanes
+      if (by_score) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        uint32_t v = key[i];
-        if (by_score) v = l[i] > -INFINITY ? ordered_bits(key_score(l[i])) : 0u;
-        m2 = max(m2, min(m1, v));
-        m1 = max(m1, v);
+        for (int i = 0; i < PER; ++i) {
+          const float v = l[i] > -INFINITY ? key_score(l[i]) : -INFINITY;
+          second = fmaxf(second, fminf(top, v));
+          top = fmaxf(top, v);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          second = fmaxf(second, fminf(top, key[i]));
+          top = fmaxf(top, key[i]);
+        }
       }
-      if (!own_group_kept(a, lane, m1, m2, per_group, biased || by_score, &margin)) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) key[i] = 0u;
+      const bool border = biased || by_score;
+      switch (a.lane_shift) {
+        case 0: kept = own_group_kept<0>(a, lane, top, second, border, &margin); break;
+        case 1: kept = own_group_kept<1>(a, lane, top, second, border, &margin); break;
+        case 2: kept = own_group_kept<2>(a, lane, top, second, border, &margin); break;
+        case 3: kept = own_group_kept<3>(a, lane, top, second, border, &margin); break;
+        default: kept = own_group_kept<4>(a, lane, top, second, border, &margin); break;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (lane * PER + i < a.E)
-          sh[lane * PER + i] = key[i] == 0u ? -INFINITY : (by_score ? key_score(l[i]) : unordered(key[i]));
+          sh[lane * PER + i] = by_score && key[i] > -INFINITY ? key_score(l[i]) : key[i];
       __syncwarp();
       const uint32_t keep = kept_groups(a, lane, [&](int e) { return sh[e]; }, &margin);
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const uint32_t e = static_cast<uint32_t>(lane * PER + i);
-        if (e >= static_cast<uint32_t>(a.E) || !((keep >> __umulhi(e, a.size_magic)) & 1u)) key[i] = 0u;
+        if (e >= static_cast<uint32_t>(a.E) || !((keep >> __umulhi(e, a.size_magic)) & 1u)) key[i] = -INFINITY;
       }
     }
-    if ((biased || by_score) && !(margin > 2.f * eps)) return false;
+    // error of a difference of two groups: one or two keys each, rounded once more where the
+    // bias is added (and their sum)
+    const float keys = a.group_top > 1 ? 2.f : 1.f;
+    if ((biased || by_score) && !(margin > keys * (eps + 2.4e-7f * (smax + bias_max)))) return false;
   }
   // a lower bound of the last key needed, from the lanes' maxima
   const int need = a.k + (biased ? 1 : 0);
-  uint32_t top = 0u;
+  if (a.G == 1 || by_score || a.lane_shift < 0) {  // (otherwise the lane's top it is)
+    top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) top = max(top, key[i]);
-  uint32_t bound = 1u;
-  for (int r = 0; r < need; ++r) {
-    const uint32_t m = __reduce_max_sync(kAll, top);
-    bound = max(m, 1u);
-    if (m == 0u) break;
-    const uint32_t who = __ballot_sync(kAll, top == m);
-    if (lane == __ffs(who) - 1) top = 0u;
+    for (int i = 0; i < PER; ++i) top = fmaxf(top, key[i]);
   }
-  // key and expert in one number: the larger key, or the lower expert, is the larger number
-  uint64_t* cand = reinterpret_cast<uint64_t*>(sh);
-  int mine_in = 0;
+  const float ranked = warp_sort_desc(kept ? top : -INFINITY, lane);
+  float bound = __shfl_sync(kAll, ranked, (need - 1) & 31);
+  bound = need > 32 ? -FLT_MAX : fmaxf(bound, -FLT_MAX);  // (none is below)
+  uint32_t in = 0u;  // a bit for each candidate
 #pragma unroll
-  for (int i = 0; i < PER; ++i) mine_in += key[i] >= bound ? 1 : 0;
+  for (int i = 0; i < PER; ++i) in |= key[i] >= bound ? 1u << i : 0u;
+  if (!kept) in = 0u;
+  const int mine_in = __popc(in);
   int at = mine_in;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -414,30 +435,51 @@ __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const floa
   }
   const int n = __shfl_sync(kAll, at, 31);
   if (n > kRsCand) return false;  // many equal keys
-  at -= mine_in;
-  if (mine_in > 0) {
+  // gathered in the order of the experts, as (key, expert)
+  uint2* cand = reinterpret_cast<uint2*>(sh);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(cand + kRsCand);
+  uint2* slot = cand + at - mine_in;
+  if (in != 0u) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (key[i] >= bound)
-        cand[at++] = (static_cast<uint64_t>(key[i]) << 32) | static_cast<uint32_t>(~(lane * PER + i));
+      if ((in >> i) & 1u) *slot++ = make_uint2(__float_as_uint(key[i]), lane * PER + i);
   }
   __syncwarp();
-  uint64_t* sorted = cand + kRsCand;
-  for (int c = lane; c < n; c += 32) {
-    const uint64_t mine = cand[c];
+  uint2 mine[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = lane + 32 * h;
+    if (c < n) {
+      mine[h] = cand[c];
+      mine[h].x = ordered_bits(__fadd_rn(__uint_as_float(mine[h].x), 0.f));  // -0 and +0 are one key
+    }
+    if (h == 0 || n > 32) keys[c] = mine[h].x;  // (0 past the last one)
+  }
+  __syncwarp();
+  // the rank of a candidate: larger keys, and equal ones before it
+  uint2* sorted = cand;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = lane + 32 * h;
+    if (h == 1 && n <= 32) break;
     int rank = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) rank += cand[j] > mine ? 1 : 0;
-    sorted[rank] = mine;
+    for (int j = 0; j < n; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(keys + j);
+      rank += o.x > mine[h].x - (j < c ? 1u : 0u) ? 1 : 0;
+      rank += o.y > mine[h].x - (j + 1 < c ? 1u : 0u) ? 1 : 0;
+      rank += o.z > mine[h].x - (j + 2 < c ? 1u : 0u) ? 1 : 0;
+      rank += o.w > mine[h].x - (j + 3 < c ? 1u : 0u) ? 1 : 0;
+    }
+    if (c < n) sorted[rank] = mine[h];
   }
   __syncwarp();
-  const uint64_t got = lane < min(n, a.k) ? sorted[lane] : 0ull;
-  const int sel = got != 0ull ? static_cast<int>(~static_cast<uint32_t>(got)) : -1;
+  const uint2 got = lane < min(n, a.k) ? sorted[lane] : make_uint2(0u, 0u);
+  const int sel = got.x != 0u ? static_cast<int>(got.y) : -1;
   if (biased) {
     bool close = false;
     if (sel >= 0 && lane + 1 < n) {
-      const float hi = unordered(static_cast<uint32_t>(got >> 32));
-      const float lo = unordered(static_cast<uint32_t>(sorted[lane + 1] >> 32));
+      const float hi = unordered(got.x);
+      const float lo = unordered(sorted[lane + 1].x);
       close = !(hi - lo > eps + 1.2e-7f * (fabsf(hi) + fabsf(lo)));
     }
     if (__any_sync(kAll, close)) return false;
@@ -446,10 +488,11 @@ __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const floa
   const bool have = sel >= 0;
   const float lj = have ? row[sel] : -INFINITY;
   float w = 0.f;
-  if (have && !(soft && a.renorm)) w = soft ? exp_below<float>(lj, lmax) / z : sigmoid_k<float>(lj);
+  if (have && !(soft && a.renorm))
+    w = soft ? exp_below<float>(lj, lmax) * smax : __fdividef(1.f, 1.f + expf(-lj));
   if (a.renorm) {
     const float sum = soft ? 0.f : warp_sum(w);
-    if (sum >= kTinySum) w /= sum;
+    if (sum >= kTinySum) w = __fdividef(w, sum);
     else w = selected_share<float>(soft, have, lj);
   }
   if (lane < a.k) {
@@ -461,7 +504,7 @@ __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const floa
 
 // A warp per row, rows in a grid stride with the next row's logits on their way.
 // Floor: 4E bytes read a row (8k written); instruction issue is what it spends its time on.
-template <int PER>
+template <int PER, int SOFT, int BIASED>
 __global__ void __launch_bounds__(kRsWarps * 32, PER <= 8 ? 8 : (PER <= 12 ? 6 : 1)) route_scored_kernel(const __grid_constant__ ScoredArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -474,8 +517,14 @@ __global__ void __launch_bounds__(kRsWarps * 32, PER <= 8 ? 8 : (PER <= 12 ? 6 :
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane * PER + i;
-    bias[i] = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+    const float b = BIASED != 0 && a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+    bias[i] = fmaxf(b, -INFINITY);  // NaN takes an expert out like -inf
   }
+  float bias_max = 0.f;  // of the finite ones
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (fabsf(bias[i]) < INFINITY) bias_max = fmaxf(bias_max, fabsf(bias[i]));
+  if (BIASED != 0) bias_max = warp_max_f(bias_max);
   auto fetch = [&](int t, float (&l)[PER]) {
     const int64_t at = static_cast<int64_t>(t) * a.E;
     const float* src = (a.n_splits > 0 ? a.partials : a.logits) + at;
@@ -517,10 +566,10 @@ __global__ void __launch_bounds__(kRsWarps * 32, PER <= 8 ? 8 : (PER <= 12 ? 6 :
     for (int i = 0; i < PER; ++i) {
       const int e = lane * PER + i;
       if (a.n_splits > 0 && e < a.E) a.logits_out[at + e] = l[i];
-      l[i] = l[i] > -INFINITY ? l[i] : -INFINITY;  // NaN is masked like -inf
+      l[i] = fmaxf(l[i], -INFINITY);  // NaN is masked like -inf
     }
     __syncwarp();  // row[sel] may be another lane's logits_out
-    if (!route_row<PER>(a, t, l, bias, row, reinterpret_cast<float*>(sh[w]))) {
+    if (!route_row<PER, SOFT, BIASED>(a, t, l, bias, bias_max, row, reinterpret_cast<float*>(sh[w]))) {
       __syncwarp();
       route_row_64<PER>(a, t, row, sh[w]);
     }
@@ -584,54 +633,75 @@ __device__ __forceinline__ void load_row(const float* row, int E, int lane, floa
   }
 }
 
-// sigmoid(l) and 1 - sigmoid(l), each to its own precision: with q = exp(-|l|), 1 / (1 + q)
-// is the larger of the two and q / (1 + q) the smaller.
-__device__ __forceinline__ void sigmoid_both(float l, float& s, float& t) {
-  const float q = __expf(-fabsf(l)), r = __fdividef(1.f, 1.f + q);
-  s = l >= 0.f ? r : q * r;
-  t = l >= 0.f ? q * r : r;
+// 2^x and 1 / x from the hardware (2^-22 and 2^-23 of the result); no result is subnormal.
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// Scores of a row up to a common factor: l holds the logits (NaN: -inf) and becomes s; t gets
-// 1 - sigmoid (sigmoid only).  Returns the sum of s over the row, 0 where it is masked as a
-// whole; lmax: the logit whose s is 1, where s is e^(l - lmax) (shifted).
+// sigmoid(l) and 1 - sigmoid(l), each to its own precision: with q = exp(-|l|), 1 / (1 + q)
+// is the larger of the two and q / (1 + q) the smaller (0 at -inf).
+__device__ __forceinline__ void sigmoid_both(float l, float& s, float& t) {
+  const float q = ex2_fast(fabsf(l) * -1.4426950408889634f), r = rcp_fast(1.f + q), o = q * r;
+  s = l >= 0.f ? r : o;
+  t = l >= 0.f ? o : r;
+}
+
+// s = e^(l - max l) of a row, and its sum (0 where the row is masked as a whole); lmax: the
+// largest logit.  l has -inf in place of a NaN.
+template <int PER>
+__device__ __forceinline__ float softmax_of_row(const float (&l)[PER], float (&s)[PER], float& lmax) {
+  lmax = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) lmax = fmaxf(lmax, l[i]);
+  lmax = warp_max_f(lmax);
+  float z = 0.f;
+  if (fabsf(lmax) < INFINITY) {
+    const float c = 1.4426950408889634f, m = lmax * c;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      s[i] = ex2_fast(fmaf(l[i], c, -m));
+      z += s[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      s[i] = l[i] == lmax && lmax > -INFINITY ? 1.f : 0.f;
+      z += s[i];
+    }
+  }
+  return warp_sum(z);
+}
+
+// Scores of a row up to a common factor: l (NaN: -inf) -> s, and t = 1 - sigmoid (sigmoid
+// only).  Returns the sum of s over the row, 0 where it is masked as a whole; shifted: s is
+// e^(l - lmax).
 // A row whose sigmoids sum to less than kTinySum has every logit below -69, where
 // sigmoid(l) = e^l to more than 32 bits: its shares are the softmax's.
 template <int PER>
-__device__ __forceinline__ float scores_of_row(bool soft, float (&s)[PER], float (&t)[PER], float& lmax,
-                                               bool& shifted) {
-  float z = 0.f;
-  lmax = -INFINITY;
-  shifted = soft;
+__device__ __forceinline__ float scores_of_row(bool soft, float (&l)[PER], float (&s)[PER], float (&t)[PER],
+                                               float& lmax, bool& shifted) {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    s[i] = s[i] > -INFINITY ? s[i] : -INFINITY;
-    lmax = fmaxf(lmax, s[i]);
-  }
+  for (int i = 0; i < PER; ++i) l[i] = fmaxf(l[i], -INFINITY);
   if (!soft) {
-    float v[PER];
+    float z = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      sigmoid_both(s[i], v[i], t[i]);
-      if (!(s[i] > -INFINITY)) v[i] = 0.f;
-      z += v[i];
+      sigmoid_both(l[i], s[i], t[i]);
+      z += s[i];
     }
     z = warp_sum(z);
-    if (z >= kTinySum) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) s[i] = v[i];
-      return z;
-    }
-    shifted = true;
+    shifted = false;
+    if (z >= kTinySum) return z;
   }
-  lmax = warp_max_f(lmax);
-  z = 0.f;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    s[i] = s[i] > -INFINITY ? (s[i] == lmax ? 1.f : __expf(s[i] - lmax)) : 0.f;
-    z += s[i];
-  }
-  return warp_sum(z);
+  shifted = true;
+  return softmax_of_row<PER>(l, s, lmax);
 }
 
 // Sequence of row t: the last q with offsets[q] <= t < offsets[q + 1], -1 outside all.
@@ -663,34 +733,31 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_backward_kernel(const __g
   const float dg = lane < a.k ? __ldg(a.dgate + static_cast<int64_t>(t) * a.k + lane) : 0.f;
   const int q = a.dscore ? sequence_of(a.seq_offsets, a.n_seq, t) : -1;
   const bool whole = q >= 0 || (soft && !a.renorm);  // scores of the whole row are needed
-  float s[PER], t1[PER], c[PER];
+  float l[PER], s[PER], t1[PER], c[PER];
   float lmax = -INFINITY, z = 0.f;
   bool shifted = soft;
   const float up = (q >= 0 && a.dloss) ? __ldg(a.dloss) : 1.f;
   const float* crow = a.dscore + static_cast<int64_t>(q >= 0 ? q : 0) * a.E;
   if (whole) {
-    load_row<PER, VEC>(row, a.E, lane, -INFINITY, s);
+    load_row<PER, VEC>(row, a.E, lane, -INFINITY, l);
     if (q >= 0) load_row<PER, VEC>(crow, a.E, lane, 0.f, c);
   }
   float lj = -INFINITY;
   if (e >= 0 && e < a.E) lj = __ldg(row + e);
   const bool have = lj > -INFINITY;
   if (!have) e = -1 - lane;  // no expert: equal to no other place
-  if (whole) z = scores_of_row<PER>(soft, s, t1, lmax, shifted);
+  if (whole) z = scores_of_row<PER>(soft, l, s, t1, lmax, shifted);
   const float inv_z = z > 0.f ? 1.f / z : 0.f;
   float csum = 0.f;  // sum c s'
   if (q >= 0) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      c[i] *= up;
-      csum = fmaf(c[i], s[i], csum);
-    }
+    for (int i = 0; i < PER; ++i) csum = fmaf(c[i], s[i], csum);
     csum = warp_sum(csum) * inv_z;
   }
   float g = have ? a.rsf * dg : 0.f;
   float sj = 0.f, tj = 0.f;  // the place's sigmoid and 1 - sigmoid
   if (!soft && have) sigmoid_both(lj, sj, tj);
-  const float mine = shifted ? (have ? (lj == lmax ? 1.f : __expf(lj - lmax)) : 0.f) : sj;
+  const float mine = shifted ? (have ? exp_below<float>(lj, lmax) : 0.f) : sj;
   float w = 0.f;  // renormalised: the place's share; otherwise its score
   if (a.renorm) {
     w = selected_share<float>(soft, have, lj);
@@ -706,8 +773,12 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_backward_kernel(const __g
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     float d = 0.f;
-    if (whole) d = s[i] * inv_z * ((q >= 0 ? c[i] - csum : 0.f) - dot);
-    if (whole && !soft) d *= t1[i];
+    if (q >= 0) {
+      d = s[i] * inv_z * fmaf(up, c[i] - csum, -dot);
+      if (!soft) d *= t1[i];
+    } else if (whole) {  // a softmax
+      d = s[i] * (inv_z * -dot);
+    }
     s[i] = d;
   }
   if constexpr (VEC) {
@@ -739,7 +810,7 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_backward_kernel(const __g
   __syncwarp();
   if (have && (same & ((1u << lane) - 1u)) == 0u) {
     float d = 0.f;
-    if (whole) d = mine * inv_z * ((q >= 0 ? up * __ldg(crow + e) - csum : 0.f) - dot);
+    if (whole) d = mine * inv_z * ((q >= 0 ? up * (__ldg(crow + e) - csum) : 0.f) - dot);
     d = fmaf(gs, w, d);
     if (!soft) d *= tj;
     if (out) out[e] = d;
@@ -856,7 +927,7 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_rows_kernel(const __gr
   for (int i = threadIdx.x; i < PER * 32; i += blockDim.x) hist[i] = 0;
   if (threadIdx.x == 0) rows_ok = 0;
   __syncthreads();
-  float acc[PER], s[PER], next[PER], t1[PER];
+  float acc[PER], l[PER], next[PER], s[PER], t1[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
   int ok = 0;
@@ -867,12 +938,12 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_rows_kernel(const __gr
     load_row<PER, VEC>(a.logits + static_cast<int64_t>(r) * a.E, a.E, lane, -INFINITY, v);
     p = lane < a.k ? __ldg(a.topk_idx + static_cast<int64_t>(r) * a.k + lane) : -1;
   };
-  if (t < hi) fetch(t, s, pick);
+  if (t < hi) fetch(t, l, pick);
   for (; t < hi; t += kBalWarps) {
     if (t + kBalWarps < hi) fetch(t + kBalWarps, next, pick_next);
     float lmax;
     bool shifted;
-    const float z = scores_of_row<PER>(soft, s, t1, lmax, shifted);
+    const float z = scores_of_row<PER>(soft, l, s, t1, lmax, shifted);
     if (z > 0.f) {
       const float inv = 1.f / z;
 #pragma unroll
@@ -881,7 +952,7 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_rows_kernel(const __gr
     }
     if (pick >= 0 && pick < a.E) atomicAdd(&hist[pick], 1);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) s[i] = next[i];
+    for (int i = 0; i < PER; ++i) l[i] = next[i];
     pick = pick_next;
   }
 #pragma unroll
@@ -949,12 +1020,13 @@ __global__ void __launch_bounds__(kBalExperts * kBalSlices) balance_finish_kerne
     shd[0][el] = d * p;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double v = 0.0;
-    for (int i = 0; i < kBalExperts; ++i) v += shd[0][i];
-    a.seq_loss[blockIdx.x] = v;
-    __threadfence();
-    last = atomicAdd(a.done, 1) == static_cast<int>(gridDim.x) - 1;
+  if (w == 0) {
+    const double v = warp_sum(shd[0][lane] + shd[0][lane + 32]);
+    if (lane == 0) {
+      a.seq_loss[blockIdx.x] = v;
+      __threadfence();
+      last = atomicAdd(a.done, 1) == static_cast<int>(gridDim.x) - 1;
+    }
   }
   __syncthreads();
   if (!last) return;
@@ -965,10 +1037,9 @@ __global__ void __launch_bounds__(kBalExperts * kBalSlices) balance_finish_kerne
   __syncthreads();
   if (lane == 0) shd[0][w] = v;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    v = 0.0;
-    for (int i = 0; i < kWarps; ++i) v += shd[0][i];
-    *a.loss = static_cast<float>(v);
+  if (w == 0) {
+    v = warp_sum(lane < kWarps ? shd[0][lane] : 0.0);
+    if (lane == 0) *a.loss = static_cast<float>(v);
   }
 }
 

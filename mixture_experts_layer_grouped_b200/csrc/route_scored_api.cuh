@@ -55,10 +55,18 @@ moe_status do_route_scored(const moe_config& c, const moe_router& r, const void*
   return by_experts(c.E, [&](auto per) -> moe_status {
     constexpr int PER = decltype(per)::value;
     const int lanes = a.size % PER == 0 ? a.size / PER : 0;
-    a.lanes_per_group = (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    a.lane_shift = -1;
+    if (lanes > 0 && (lanes & (lanes - 1)) == 0)
+      for (a.lane_shift = 0; (1 << a.lane_shift) < lanes;) ++a.lane_shift;
+    // the form is compiled in where rows are short enough that its branches show
+    auto kern = route_scored_kernel<PER, -1, -1>;
+    if constexpr (PER == 8 || PER == 12) {
+      kern = r.score == MOE_SCORE_SOFTMAX
+                 ? (bias ? route_scored_kernel<PER, 1, 1> : route_scored_kernel<PER, 1, 0>)
+                 : (bias ? route_scored_kernel<PER, 0, 1> : route_scored_kernel<PER, 0, 0>);
+    }
     const int want = (c.T + kRsWarps - 1) / kRsWarps, most = sm_count() * 8;
-    MOE_TRY(launch_pdl(route_scored_kernel<PER>, dim3(want < most ? want : most),
-                       dim3(kRsWarps * 32), 0, s, a));
+    MOE_TRY(launch_pdl(kern, dim3(want < most ? want : most), dim3(kRsWarps * 32), 0, s, a));
     return launch_check();
   });
 }
