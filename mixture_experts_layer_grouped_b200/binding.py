@@ -470,70 +470,83 @@ def moe_backward(cfg, weights, bwd_weights, saved: dict, dy, dx, workspace, dlog
     if router is None:
         _check("moe_backward", lib().moe_backward(ctypes.byref(cfg), *first, *last))
         return
-    off, n_seq = _sequences(seq_offsets)
+    dev = _device()
+    off, n_seq = _sequences(seq_offsets, dev)
     _check("moe_backward_scored", lib().moe_backward_scored(
         ctypes.byref(cfg), ctypes.byref(router), *first,
-        _sized(dscore, f32, (n_seq, cfg.E), "dscore"), off, n_seq, _sized(dloss, f32, (1,), "dloss"),
+        _sized(dscore, f32, (n_seq, cfg.E), "dscore", dev), off, n_seq,
+        _sized(dloss, f32, (1,), "dloss", dev),
         *last))
 
 
-def _sized(t, dtype, shape, name):
-    """The address of a tensor of this type and shape, contiguous on the current device (the C
-    call sees only the address); None for None."""
+def _sized(t, dtype, shape, name, dev):
+    """The address of a tensor of this type and shape, contiguous on the current device ``dev``
+    (the C call sees only the address); None for None."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
-        dev = t.get_device()  # -1: host memory
-        if dev >= 0 and dev == torch._C._cuda_getDevice():
-            return t.data_ptr()
-    where = "" if not t.is_cuda else f", current device cuda:{torch.cuda.current_device()}"
-    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on the "
-                     f"current CUDA device, got {t.dtype} of shape {tuple(t.shape)} on {t.device} "
-                     f"(contiguous={t.is_contiguous()}{where})")
+    if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+            and dev >= 0):
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                     f"cuda:{dev} (the current device), got {t.dtype} of shape {tuple(t.shape)} "
+                     f"on {t.device} (contiguous={t.is_contiguous()})")
 
 
-def _scratch(workspace):
-    """Address and bytes of a workspace."""
+def _device():
+    """The current device's index, -1 without CUDA."""
+    try:
+        return torch._C._cuda_getDevice()
+    except (RuntimeError, AttributeError):
+        return -1
+
+
+def _scratch(workspace, dev):
+    """Address and bytes of a workspace (a byte tensor of new_workspace)."""
     if workspace is None:
         return None, 0
-    return workspace.data_ptr(), workspace.numel()
+    n = workspace.numel()
+    return _sized(workspace, torch.uint8, (n,), "workspace", dev), n
 
 
 def moe_route_scored(cfg, router, topk_idx, topk_w, x=None, w_router=None, bias=None,
                      workspace=None, logits_in=None, logits_out=None, stream=None):
     """Routing by softmax or sigmoid scores: from x and w_router (with a workspace and
     logits_out), or from the logits alone (logits_in)."""
+    dev = _device()
     bf, f32, T, E, k = torch.bfloat16, torch.float32, cfg.T, cfg.E, cfg.top_k
     _call(
-        "moe_route_scored", cfg, router, _sized(x, bf, (T, cfg.H), "x"),
-        _sized(w_router, bf, (E, cfg.H), "w_router"), _sized(bias, f32, (E,), "bias"),
-        _sized(logits_in, f32, (T, E), "logits_in"),
-        _sized(logits_out, f32, (T, E), "logits_out"),
-        _sized(topk_idx, torch.int32, (T, k), "topk_idx"), _sized(topk_w, f32, (T, k), "topk_w"),
-        *_scratch(workspace), _stream(stream))
+        "moe_route_scored", cfg, router, _sized(x, bf, (T, cfg.H), "x", dev),
+        _sized(w_router, bf, (E, cfg.H), "w_router", dev), _sized(bias, f32, (E,), "bias", dev),
+        _sized(logits_in, f32, (T, E), "logits_in", dev),
+        _sized(logits_out, f32, (T, E), "logits_out", dev),
+        _sized(topk_idx, torch.int32, (T, k), "topk_idx", dev),
+        _sized(topk_w, f32, (T, k), "topk_w", dev),
+        *_scratch(workspace, dev), _stream(stream))
 
 
-def _sequences(seq_offsets):
+def _sequences(seq_offsets, dev):
     """Address and number of the sequences that the offsets bound (None: one of all rows)."""
     if seq_offsets is None:
         return None, 1
     if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
         raise ValueError("seq_offsets: expected at least two offsets in one dimension")
     n = seq_offsets.numel()
-    return _sized(seq_offsets, torch.int32, (n,), "seq_offsets"), n - 1
+    return _sized(seq_offsets, torch.int32, (n,), "seq_offsets", dev), n - 1
 
 
 def moe_route_backward(cfg, router, logits, topk_idx, dgate, dlogits, dscore=None,
                        seq_offsets=None, dloss=None, stream=None):
     """dgate -> dlogits of the scored router; with ``dscore`` (of moe_balance_loss, for the
     same ``seq_offsets``) plus the balance loss's gradient, times the device scalar ``dloss``."""
+    dev = _device()
     f32, T, E, k = torch.float32, cfg.T, cfg.E, cfg.top_k
-    off, n_seq = _sequences(seq_offsets)
+    off, n_seq = _sequences(seq_offsets, dev)
     _call(
-        "moe_route_backward", cfg, router, _sized(logits, f32, (T, E), "logits"),
-        _sized(topk_idx, torch.int32, (T, k), "topk_idx"), _sized(dgate, f32, (T, k), "dgate"),
-        _sized(dscore, f32, (n_seq, E), "dscore"), off, n_seq, _sized(dloss, f32, (1,), "dloss"),
-        _sized(dlogits, f32, (T, E), "dlogits"), _stream(stream))
+        "moe_route_backward", cfg, router, _sized(logits, f32, (T, E), "logits", dev),
+        _sized(topk_idx, torch.int32, (T, k), "topk_idx", dev),
+        _sized(dgate, f32, (T, k), "dgate", dev), _sized(dscore, f32, (n_seq, E), "dscore", dev),
+        off, n_seq, _sized(dloss, f32, (1,), "dloss", dev),
+        _sized(dlogits, f32, (T, E), "dlogits", dev), _stream(stream))
 
 
 def moe_balance_workspace_size(cfg, n_seq=1) -> int:
@@ -546,13 +559,14 @@ def moe_balance_workspace_size(cfg, n_seq=1) -> int:
 def moe_balance_loss(cfg, router, logits, topk_idx, coef, loss, load, dscore, workspace,
                      seq_offsets=None, stream=None):
     """Balance loss [1], load [n_seq, E] and dscore [n_seq, E] of the routed rows."""
+    dev = _device()
     f32, i32, T, E = torch.float32, torch.int32, cfg.T, cfg.E
-    off, n_seq = _sequences(seq_offsets)
+    off, n_seq = _sequences(seq_offsets, dev)
     _call(
-        "moe_balance_loss", cfg, router, _sized(logits, f32, (T, E), "logits"),
-        _sized(topk_idx, i32, (T, cfg.top_k), "topk_idx"), off, n_seq, coef,
-        _sized(loss, f32, (1,), "loss"), _sized(load, i32, (n_seq, E), "load"),
-        _sized(dscore, f32, (n_seq, E), "dscore"), *_scratch(workspace), _stream(stream))
+        "moe_balance_loss", cfg, router, _sized(logits, f32, (T, E), "logits", dev),
+        _sized(topk_idx, i32, (T, cfg.top_k), "topk_idx", dev), off, n_seq, coef,
+        _sized(loss, f32, (1,), "loss", dev), _sized(load, i32, (n_seq, E), "load", dev),
+        _sized(dscore, f32, (n_seq, E), "dscore", dev), *_scratch(workspace, dev), _stream(stream))
 
 
 GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -565,35 +579,39 @@ def moe_muon_workspace_size(mcfg) -> int:
     return n.value
 
 
-def _stacked(mcfg, t, dtype, name):
+def _stacked(mcfg, t, dtype, name, dev):
     """A contiguous stack of the config's matrices (a single matrix may be 2-D)."""
     shape = (mcfg.groups, mcfg.rows, mcfg.cols)
-    return _sized(t, dtype, shape[1:] if mcfg.groups == 1 and t.dim() == 2 else shape, name)
+    return _sized(t, dtype, shape[1:] if mcfg.groups == 1 and t.dim() == 2 else shape, name, dev)
 
 
-def _grad(mcfg, t, name):
+def _grad(mcfg, t, name, dev):
     if t.dtype not in GRAD_DTYPES:
         raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
-    return _stacked(mcfg, t, t.dtype, name), GRAD_DTYPES[t.dtype]
+    return _stacked(mcfg, t, t.dtype, name, dev), GRAD_DTYPES[t.dtype]
 
 
 def moe_orthogonalize(mcfg, g, out, workspace, stream=None):
     """out (bf16) = each matrix of g (fp32 or bf16) with its singular values moved to about 1."""
+    dev = _device()
     _call(
-        "moe_orthogonalize", mcfg, *_grad(mcfg, g, "g"), _stacked(mcfg, out, torch.bfloat16, "out"),
-        *_scratch(workspace), _stream(stream))
+        "moe_orthogonalize", mcfg, *_grad(mcfg, g, "g", dev),
+        _stacked(mcfg, out, torch.bfloat16, "out", dev),
+        *_scratch(workspace, dev), _stream(stream))
 
 
 def moe_muon_step(mcfg, grad, momentum, momentum_out, w, w_out, workspace, beta=0.95,
                   nesterov=True, step=0.02, decay=0.0, stream=None):
     """Momentum, orthogonalised update and weights of one optimiser step; ``momentum_out`` may
     be ``momentum`` and ``w_out`` may be ``w``."""
+    dev = _device()
     f32, bf = torch.float32, torch.bfloat16
     _call(
-        "moe_muon_step", mcfg, *_grad(mcfg, grad, "grad"), _stacked(mcfg, momentum, f32, "momentum"),
-        _stacked(mcfg, momentum_out, f32, "momentum_out"), beta, 1 if nesterov else 0,
-        _stacked(mcfg, w, bf, "w"), _stacked(mcfg, w_out, bf, "w_out"), step, decay,
-        *_scratch(workspace), _stream(stream))
+        "moe_muon_step", mcfg, *_grad(mcfg, grad, "grad", dev),
+        _stacked(mcfg, momentum, f32, "momentum", dev),
+        _stacked(mcfg, momentum_out, f32, "momentum_out", dev), beta, 1 if nesterov else 0,
+        _stacked(mcfg, w, bf, "w", dev), _stacked(mcfg, w_out, bf, "w_out", dev), step, decay,
+        *_scratch(workspace, dev), _stream(stream))
 
 
 class MoELayer:

@@ -760,7 +760,9 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_backward_kernel(const __g
   const float mine = shifted ? (have ? exp_below<float>(lj, lmax) : 0.f) : sj;
   float w = 0.f;  // renormalised: the place's share; otherwise its score
   if (a.renorm) {
-    w = selected_share<float>(soft, have, lj);
+    const float sum = soft ? 0.f : warp_sum(sj);
+    if (sum >= kTinySum) w = __fdividef(sj, sum);
+    else w = selected_share<float>(soft, have, lj);
     const float gw = warp_sum(g * w);
     if (have) g -= gw;
   } else if (have) {
@@ -798,17 +800,18 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_backward_kernel(const __g
     for (int ee = lane + 32 * PER; ee < a.ld_b - a.col_b; ee += 32) brow[ee] = __float2bfloat16_rn(0.f);
   // the selected ones over it (the warp's stores above come first); places that name the
   // same expert add up
-  const unsigned same = __match_any_sync(kAll, e);
-  float gs = g;
-  if (__any_sync(kAll, have && (same & (same - 1)) != 0u)) {
-    gs = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-      const float o = __shfl_sync(kAll, g, j);
-      if ((same >> j) & 1u) gs += o;
+  float gs = 0.f;
+  bool first = true;
+  for (int j = 0; j < a.k; ++j) {
+    const int ej = __shfl_sync(kAll, e, j);
+    const float gj = __shfl_sync(kAll, g, j);
+    if (ej == e) {
+      gs += gj;
+      if (j < lane) first = false;
     }
   }
   __syncwarp();
-  if (have && (same & ((1u << lane) - 1u)) == 0u) {
+  if (have && first) {
     float d = 0.f;
     if (whole) d = mine * inv_z * ((q >= 0 ? up * (__ldg(crow + e) - csum) : 0.f) - dot);
     d = fmaf(gs, w, d);

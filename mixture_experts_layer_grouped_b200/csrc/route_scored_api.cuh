@@ -127,8 +127,8 @@ struct BalanceLayout {
 
 BalanceLayout balance_layout(const moe_config& c, int32_t n_seq) {
   BalanceLayout L;
-  // rows a block: one per warp until the blocks fill the GPU twice, at most 128
-  int rows = (c.T / (2 * 148) + kBalWarps - 1) / kBalWarps * kBalWarps;
+  // rows a block: one a warp until the blocks fill the GPU, at most 128
+  int rows = (c.T / 148 + kBalWarps - 1) / kBalWarps * kBalWarps;
   L.tile_rows = rows < kBalWarps ? kBalWarps : (rows > 128 ? 128 : rows);
   L.tiles = static_cast<int>((static_cast<int64_t>(c.T) + L.tile_rows - 1) / L.tile_rows) + n_seq;
   const size_t n = static_cast<size_t>(L.tiles) * c.E * 4;
