@@ -69,15 +69,17 @@ __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 // Momentum and each chunk's sum of u^2, in 64 bits (the squares of 1e-30 or 1e30 stay in
-// range), added in an order fixed by the shape.  VEC: four elements an access.
+// range), added in an order fixed by the shape.  VEC: four elements an access, four accesses
+// in flight (mom_out may be mom_in, so the compiler may not move loads over stores itself).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) muon_norm_kernel(const __grid_constant__ MuonInArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ double red[8];
-  if (blockIdx.x == 0 && blockIdx.y == 0)
+  const int mat = blockIdx.y;
+  if (blockIdx.x == 0 && mat == 0)
     for (int i = threadIdx.x; i < a.n_counters; i += 256) a.counters[i] = 0;
-  const int64_t base = static_cast<int64_t>(blockIdx.y) * a.n;
+  const int64_t base = static_cast<int64_t>(mat) * a.n;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
   const int64_t i1 = min(i0 + a.chunk, a.n);
   const T* g = static_cast<const T*>(a.grad) + base;
@@ -88,17 +90,27 @@ __global__ void __launch_bounds__(256) muon_norm_kernel(const __grid_constant__ 
     return a.nesterov ? fmaf(a.beta, mo, gv) : mo;
   };
   if constexpr (VEC) {
-    for (int64_t i = i0 + threadIdx.x * 4; i < i1; i += 1024) {
-      const float4 gv = load4<T>(g + i);
-      float4 mv = make_float4(0, 0, 0, 0), mo = mv, u;
-      if (a.mom_in) mv = *reinterpret_cast<const float4*>(a.mom_in + base + i);
-      u.x = one(gv.x, mv.x, mo.x);
-      u.y = one(gv.y, mv.y, mo.y);
-      u.z = one(gv.z, mv.z, mo.z);
-      u.w = one(gv.w, mv.w, mo.w);
-      if (a.mom_in) *reinterpret_cast<float4*>(a.mom_out + base + i) = mo;
-      s += static_cast<double>(u.x) * u.x + static_cast<double>(u.y) * u.y +
-           static_cast<double>(u.z) * u.z + static_cast<double>(u.w) * u.w;
+    for (int64_t j = i0 + threadIdx.x * 4; j < i1; j += 4096) {
+      float4 gv[4], mv[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = j + k * 1024;
+        gv[k] = mv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < i1) gv[k] = load4<T>(g + i);
+        if (i < i1 && a.mom_in) mv[k] = __ldcs(reinterpret_cast<const float4*>(a.mom_in + base + i));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = j + k * 1024;
+        float4 mo, u;
+        u.x = one(gv[k].x, mv[k].x, mo.x);
+        u.y = one(gv[k].y, mv[k].y, mo.y);
+        u.z = one(gv[k].z, mv[k].z, mo.z);
+        u.w = one(gv[k].w, mv[k].w, mo.w);
+        if (a.mom_in && i < i1) *reinterpret_cast<float4*>(a.mom_out + base + i) = mo;
+        s += static_cast<double>(u.x) * u.x + static_cast<double>(u.y) * u.y +
+             static_cast<double>(u.z) * u.z + static_cast<double>(u.w) * u.w;
+      }
     }
   } else {
     for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
@@ -115,7 +127,7 @@ __global__ void __launch_bounds__(256) muon_norm_kernel(const __grid_constant__ 
   if (threadIdx.x == 0) {
     s = 0.0;
     for (int i = 0; i < 8; ++i) s += red[i];
-    a.part[static_cast<int64_t>(blockIdx.y) * a.chunks + blockIdx.x] = s;
+    a.part[static_cast<int64_t>(mat) * a.chunks + blockIdx.x] = s;
   }
 }
 
@@ -130,10 +142,11 @@ __global__ void __launch_bounds__(256) muon_scale_kernel(const __grid_constant__
   pdl_wait();
   pdl_trigger();
   __shared__ double red[8];
-  const int64_t base = static_cast<int64_t>(blockIdx.y) * a.n;
+  const int mat = blockIdx.y;
+  const int64_t base = static_cast<int64_t>(mat) * a.n;
   double s = 0.0;
   for (int i = threadIdx.x; i < a.chunks; i += 256)
-    s += a.part[static_cast<int64_t>(blockIdx.y) * a.chunks + i];
+    s += a.part[static_cast<int64_t>(mat) * a.chunks + i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane_id() == 0) red[warp_id()] = s;
@@ -146,24 +159,34 @@ __global__ void __launch_bounds__(256) muon_scale_kernel(const __grid_constant__
   const T* g = static_cast<const T*>(a.grad) + base;
   const float* m = a.mom_in ? a.mom_out + base : nullptr;
   const int rows = static_cast<int>(a.n / a.cols);
-  const int64_t xb = static_cast<int64_t>(blockIdx.y) * rows * a.ld;
+  const int64_t xb = static_cast<int64_t>(mat) * rows * a.ld;
   auto one = [&](float gv, float mo) -> float {
     return scale * (!m ? gv : (a.nesterov ? fmaf(a.beta, mo, gv) : mo));
   };
   if constexpr (VEC) {
-    for (int64_t i = i0 + threadIdx.x * 4; i < i1; i += 1024) {
-      float4 gv = make_float4(0, 0, 0, 0), mo = gv;
-      if (!m || a.nesterov) gv = load4<T>(g + i);
-      if (m) mo = *reinterpret_cast<const float4*>(m + i);
-      __align__(8) __half h[4], l[4];
-      split_half(one(gv.x, mo.x), h[0], l[0]);
-      split_half(one(gv.y, mo.y), h[1], l[1]);
-      split_half(one(gv.z, mo.z), h[2], l[2]);
-      split_half(one(gv.w, mo.w), h[3], l[3]);
-      const uint32_t r = static_cast<uint32_t>(i) / static_cast<uint32_t>(a.cols);
-      const int64_t o = xb + static_cast<int64_t>(r) * a.ld + (i - static_cast<int64_t>(r) * a.cols);
-      *reinterpret_cast<uint2*>(a.hi + o) = *reinterpret_cast<const uint2*>(h);
-      *reinterpret_cast<uint2*>(a.lo + o) = *reinterpret_cast<const uint2*>(l);
+    for (int64_t j = i0 + threadIdx.x * 4; j < i1; j += 4096) {
+      float4 gv[4], mo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = j + k * 1024;
+        gv[k] = mo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < i1 && (!m || a.nesterov)) gv[k] = load4<T>(g + i);
+        if (i < i1 && m) mo[k] = *reinterpret_cast<const float4*>(m + i);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = j + k * 1024;
+        __align__(8) __half h[4], l[4];
+        split_half(one(gv[k].x, mo[k].x), h[0], l[0]);
+        split_half(one(gv[k].y, mo[k].y), h[1], l[1]);
+        split_half(one(gv[k].z, mo[k].z), h[2], l[2]);
+        split_half(one(gv[k].w, mo[k].w), h[3], l[3]);
+        if (i >= i1) continue;
+        const uint32_t r = static_cast<uint32_t>(i) / static_cast<uint32_t>(a.cols);
+        const int64_t o = xb + static_cast<int64_t>(r) * a.ld + (i - static_cast<int64_t>(r) * a.cols);
+        __stcs(reinterpret_cast<uint2*>(a.hi + o), *reinterpret_cast<const uint2*>(h));
+        __stcs(reinterpret_cast<uint2*>(a.lo + o), *reinterpret_cast<const uint2*>(l));
+      }
     }
   } else {
     for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
@@ -193,8 +216,7 @@ constexpr int kNsSets = 4;                   // at most, of one to three arrays 
 constexpr int kNsMaxSplits = 8;
 constexpr int kNsSmemBytes = kNsStages * 2 * kNsOpBytes + kNsEpiWarps * (kNsWarpBytes + 32 * 4) + 768 + 1024;
 
-// Work units in order: for each run of `chunk` matrices, for each step, the Gram tiles
-// (`splits` units each, and with more than one `sums` units that add them up), the
+// Work units in order: for each step, the Gram tiles of all matrices (`splits` units each, and with more than one `sums` units that add them up), the
 // polynomial's tiles, the application's tiles.  Symmetric results: only tiles on and above
 // the diagonal.  CTAs (or pairs) claim units in this order, so what a
 // claimed unit waits for was claimed before by a running CTA, and every wait ends.
@@ -206,7 +228,7 @@ struct NsParams {
   // blocks of the epilogue (box 32 x 32, 64-byte swizzle)
   CUtensorMap x_blk[2][2], ab_blk[2][2];
   CUtensorMap out_map, w_map;  // last application, if tma_out
-  int32_t groups, rows, cols, r, steps, chunk;
+  int32_t groups, rows, cols, r, steps;
   int32_t sym_tiles, sym_n, app_tiles, app_n;  // tiles a matrix (n: tiles along a side, along columns)
   int32_t k_gram, k_r;                         // 64-wide steps of the contractions
   int32_t splits, sums;                        // sums: 0 with one split
@@ -232,12 +254,9 @@ template <int TILE>
 __device__ __forceinline__ NsUnit ns_decode(const NsParams& p, int u) {
   NsUnit t;
   const int per = p.sym_tiles * (p.splits + p.sums + 1) + p.app_tiles;  // units a matrix and step
-  const int64_t run = static_cast<int64_t>(p.chunk) * per * p.steps;
-  const int q = static_cast<int>(u / run);
-  int v = static_cast<int>(u - q * run);
-  const int first = q * p.chunk, n = min(p.chunk, p.groups - first);
-  t.k = v / (n * per);
-  v -= t.k * n * per;
+  const int n = p.groups;
+  t.k = u / (n * per);
+  int v = u - t.k * n * per;
   t.split = 0;
   if (v < n * p.sym_tiles * p.splits) {
     t.mode = kNsGram;
@@ -261,7 +280,6 @@ __device__ __forceinline__ NsUnit ns_decode(const NsParams& p, int u) {
     t.g = v / p.app_tiles;
     t.tile = v - t.g * p.app_tiles;
   }
-  t.g += first;
   if (t.mode == kNsApply) {
     t.m0 = t.tile / p.app_n;
     t.n0 = (t.tile - t.m0 * p.app_n) * TILE;

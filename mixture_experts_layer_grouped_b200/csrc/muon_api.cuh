@@ -97,9 +97,8 @@ MuonLayout muon_layout(const moe_muon_config& c) {
   L.r = c.rows < c.cols ? c.rows : c.cols;
   L.ld = (c.cols + 7) / 8 * 8;
   L.ldr = (L.r + 7) / 8 * 8;
-  // at most 256 partial sums a matrix, each of at least 4096 elements
-  int64_t chunk = ((n + 255) / 256 + 1023) / 1024 * 1024;
-  if (chunk < 4096) chunk = 4096;
+  // at most 1024 partial sums a matrix, each of whole 4096 elements (a CTA's four accesses)
+  const int64_t chunk = ((n + 1023) / 1024 + 4095) / 4096 * 4096;
   L.chunk = static_cast<int>(chunk);
   L.chunks = static_cast<int>((n + chunk - 1) / chunk);
   const bool split = muon_split(c);
@@ -183,7 +182,7 @@ moe_status launch_ns(const NsParams& p, cudaStream_t s) {
   MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmemBytes));
   int ctas = sm_count() / (PAIR ? 2 : 1);
   // no more than one product of the whole stack keeps busy: a CTA that meets every product
-  // has its instructions at hand (5 x [333, 215]: 199 us with 74 pairs, XXX with 10)
+  // has its instructions at hand (5 x [333, 215]: 199 us with 74 pairs, 195 with 10)
   const int64_t most = static_cast<int64_t>(p.groups) * std::max(p.sym_tiles * p.splits, p.app_tiles);
   if (most < ctas) ctas = static_cast<int>(most);
   cudaLaunchConfig_t cfg = {};
@@ -259,7 +258,6 @@ moe_status ns_steps(const moe_muon_config& c, const MuonArgs& u, const MuonLayou
   p.cols = c.cols;
   p.r = L.r;
   p.steps = c.steps;
-  p.chunk = c.groups;
   p.sym_tiles = L.sym_tiles;
   p.sym_n = L.sym_n;
   p.app_tiles = L.app_tiles;

@@ -14,9 +14,9 @@
 //   gate      rsf * s_e, divided by the sum over the selected when renormalised.
 //
 // The selection is that of exact arithmetic as far as 64 bits resolve it: keys are
-// computed in 32 bits with a known error, and a row in which two neighbours of the
-// sorted keys, or the groups on both sides of the border, are nearer than that error
-// is done again in 64 bits (measured at 256 experts, top 8 and a bias: under 1% of rows).
+// computed in 32 bits with a known error, and where two neighbours of the sorted keys, or
+// the groups on both sides of the border, are nearer than that error, the keys that can
+// matter there are computed again in 64 bits (at 384 experts, top 8 and a bias 2 rows in 1000).
 #pragma once
 
 #include <cfloat>
@@ -220,7 +220,24 @@ __device__ __forceinline__ uint32_t kept_groups(const ScoredArgs& a, int lane, F
   return keep_of_tops(a, lane, m1, m2, lpg, margin);
 }
 
-// One row in 64 bits by one warp, for the rows whose 32-bit keys do not tell the selection:
+// A softmax's sum over the row and a score, in 64 bits: calls and loops, not unrolled, since
+// what a rare row pays for is mostly the instructions' way into the SM.
+__device__ __noinline__ double sum_64(const float* row, int E, int lane, float lmax) {
+  double z = 0.0;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) {
+    const float v = row[e];
+    if (v > -INFINITY) z += exp_below<double>(v, lmax);
+  }
+  return warp_sum(z);
+}
+__device__ __noinline__ double score_64(bool soft, float l, float lmax, double z) {
+  const double x = exp(soft ? (l == lmax ? 0.0 : static_cast<double>(l) - lmax) : -static_cast<double>(l));
+  return soft ? x / z : 1.0 / (1.0 + x);
+}
+
+// One row in 64 bits by one warp, for the rows with more candidates than route_row holds (many
+// equal keys) and those of groups that are not whole lanes and too near each other:
 // lane i holds the PER consecutive logits from i * PER on.  k rounds of a warp maximum.
 template <int PER>
 __device__ __noinline__ void route_row_64(const ScoredArgs& a, int t, const float* row, double* sh) {
@@ -325,15 +342,18 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
 
 constexpr int kRsCand = 64;  // candidates of a row
 
+// Top k: the k-th largest of the lanes' maxima is at most the k-th largest key, so the keys
+// from it on (less their error, with a bias) are few and hold the selection; they are gathered
+// through shared memory, one or two a lane, and each finds its rank by comparing itself to all.
+// That takes about half the instructions of k rounds of maximum and removal.
+//
+// Keys nearer to each other than their error: 64 bits for the two largest of each lane (groups)
+// or for the candidates alone.  (The whole row in 64 bits: 17 us for 1024 rows of 384 logits,
+// in nearly every batch of which there is such a row, against 8.)
+//
 // One row in 32 bits by one warp; lane i holds the PER consecutive logits from i * PER on
 // (-inf past the last expert, and in place of a NaN).  Returns false, without having written
-// anything, where 32-bit keys cannot tell the selection.
-//
-// Top k: the k-th largest of the lanes' maxima is at most the k-th largest key, so the keys
-// from it on are few (k and a few more) and hold the selection; they are gathered through
-// shared memory, one or two a lane, and each finds its rank by comparing itself to all.
-// That takes about half the instructions of k rounds of maximum and removal (and one round
-// more with a bias, whose next key the border check needs).
+// anything, where it cannot tell the selection.
 // SOFT, BIASED: the form, 0 or 1, or -1 where it is asked for row by row.
 template <int PER, int SOFT, int BIASED>
 __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const float (&l)[PER],
@@ -363,6 +383,8 @@ __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const floa
   // error of such a score, doubled, relative to the row's largest: the exponential's and the
   // division's roundings, and for a softmax the sum's (PER + 5 additions)
   const float eps = (soft ? 8e-6f : 1e-6f) * smax;
+  // of a difference of two keys: the score's, and the roundings of sums with the bias
+  const float near = eps + 2.4e-7f * (smax + bias_max);
   float key[PER];  // -inf: none (a bias that takes an expert out is -inf)
 #pragma unroll
   for (int i = 0; i < PER; ++i) key[i] = biased ? (l[i] > -INFINITY ? key_score(l[i]) + bias[i] : -INFINITY) : l[i];
@@ -407,21 +429,38 @@ __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const floa
         if (e >= static_cast<uint32_t>(a.E) || !((keep >> __umulhi(e, a.size_magic)) & 1u)) key[i] = -INFINITY;
       }
     }
-    // error of a difference of two groups: one or two keys each, rounded once more where the
-    // bias is added (and their sum)
-    const float keys = a.group_top > 1 ? 2.f : 1.f;
-    if ((biased || by_score) && !(margin > keys * (eps + 2.4e-7f * (smax + bias_max)))) return false;
+    // a group has one or two keys
+    if ((biased || by_score) && !(margin > (a.group_top > 1 ? 2.f : 1.f) * near)) {
+      if (a.lane_shift < 0) return false;
+      const float from = (a.group_top > 1 ? second : top) - near;
+      uint32_t again = 0u;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float v = by_score && key[i] > -INFINITY ? key_score(l[i]) : key[i];
+        again |= v > -INFINITY && v >= from ? 1u << i : 0u;
+      }
+      const double z64 = soft ? sum_64(row, a.E, lane, lmax) : 1.0;
+      double m1 = -INFINITY, m2 = -INFINITY;
+      for (; again != 0u; again &= again - 1) {
+        const int e = lane * PER + __ffs(again) - 1;
+        const double v = score_64(soft, row[e], lmax, z64) + (biased ? static_cast<double>(__ldg(a.bias + e)) : 0.0);
+        m2 = fmax(m2, fmin(m1, v));
+        m1 = fmax(m1, v);
+      }
+      __syncwarp();
+      kept = (keep_of_tops<double>(a, lane, m1, m2, 1 << a.lane_shift, nullptr) >> (lane >> a.lane_shift)) & 1u;
+    }
   }
   // a lower bound of the last key needed, from the lanes' maxima
-  const int need = a.k + (biased ? 1 : 0);
   if (a.G == 1 || by_score || a.lane_shift < 0) {  // (otherwise the lane's top it is)
     top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) top = fmaxf(top, key[i]);
   }
   const float ranked = warp_sort_desc(kept ? top : -INFINITY, lane);
-  float bound = __shfl_sync(kAll, ranked, (need - 1) & 31);
-  bound = need > 32 ? -FLT_MAX : fmaxf(bound, -FLT_MAX);  // (none is below)
+  float bound = __shfl_sync(kAll, ranked, a.k - 1);
+  if (biased) bound -= near;
+  bound = fmaxf(bound, -FLT_MAX);  // (none is below)
   uint32_t in = 0u;  // a bit for each candidate
 #pragma unroll
   for (int i = 0; i < PER; ++i) in |= key[i] >= bound ? 1u << i : 0u;
@@ -474,7 +513,7 @@ __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const floa
   }
   __syncwarp();
   const uint2 got = lane < min(n, a.k) ? sorted[lane] : make_uint2(0u, 0u);
-  const int sel = got.x != 0u ? static_cast<int>(got.y) : -1;
+  int sel = got.x != 0u ? static_cast<int>(got.y) : -1;
   if (biased) {
     bool close = false;
     if (sel >= 0 && lane + 1 < n) {
@@ -482,7 +521,29 @@ __device__ __forceinline__ bool route_row(const ScoredArgs& a, int t, const floa
       const float lo = unordered(sorted[lane + 1].x);
       close = !(hi - lo > eps + 1.2e-7f * (fabsf(hi) + fabsf(lo)));
     }
-    if (__any_sync(kAll, close)) return false;
+    if (__any_sync(kAll, close)) {
+      const double z64 = soft ? sum_64(row, a.E, lane, lmax) : 1.0;
+      __syncwarp();  // sorted and keys are read
+      double* keys64 = reinterpret_cast<double*>(cand);
+      int* order = reinterpret_cast<int*>(keys);
+      double v[2] = {0.0, 0.0};
+      for (int c = lane, h = 0; c < n; c += 32, ++h) {
+        const int e = static_cast<int>(h == 0 ? mine[0].y : mine[1].y);
+        const double x = score_64(soft, row[e], lmax, z64) + static_cast<double>(__ldg(a.bias + e));
+        if (h == 0) v[0] = x; else v[1] = x;
+        keys64[c] = x;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = lane + 32 * h;
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += keys64[j] > v[h] || (keys64[j] == v[h] && j < c) ? 1 : 0;
+        if (c < n) order[rank] = static_cast<int>(mine[h].y);
+      }
+      __syncwarp();
+      sel = lane < min(n, a.k) ? order[lane] : -1;
+    }
   }
   // gates: lane j has place j
   const bool have = sel >= 0;
@@ -763,8 +824,11 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_backward_kernel(const __g
     const float sum = soft ? 0.f : warp_sum(sj);
     if (sum >= kTinySum) w = __fdividef(sj, sum);
     else w = selected_share<float>(soft, have, lj);
-    const float gw = warp_sum(g * w);
-    if (have) g -= gw;
+    // g_j - sum_i g_i w_i as sum_i w_i (g_j - g_i): a share near one does not cancel, and a
+    // single place's gradient is zero
+    float d = 0.f;
+    for (int i = 0; i < a.k; ++i) d = fmaf(__shfl_sync(kAll, w, i), g - __shfl_sync(kAll, g, i), d);
+    g = have ? d : 0.f;
   } else if (have) {
     w = soft ? mine * inv_z : sj;
   }

@@ -110,7 +110,7 @@ def check_selection(M, T, E, k, G, g, score, top, bias, x):
     for t in range(T):
         s = TO.scores(x[t].numpy(), score)
         d = 4 * (E + 8) * 2.0 ** -53 * s.max()
-        key = s + bias.numpy().astype(np.float64)
+        key = s + (0.0 if bias is None else bias.numpy().astype(np.float64))
         total = np.array([sum(sorted(v)[::-1][:top]) for v in key.reshape(G, -1)])
         border = np.sort(total)[::-1][g - 1]
         mine = idx[t]
@@ -135,6 +135,59 @@ def test_route_near_ties_are_decided_in_64_bits(M, score):
         bias = torch.from_numpy((s[t].max() - s[t]).astype(np.float32))
         check_selection(M, T, E, 8, 1, 1, score, 1, bias, x)
         check_selection(M, T, E, 8, 8, 3, score, 2, bias, x)
+
+
+@pytest.mark.parametrize("E,G,g", [(48, 1, 1), (64, 8, 4), (256, 8, 3), (384, 8, 4), (512, 16, 8)])
+@pytest.mark.parametrize("score", [0, 1])
+def test_route_many_near_ties(M, E, G, g, score):
+    """The same with several experts a lane, and with more than 32 keys within the error of
+    the last one selected."""
+    T = 40
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(E))
+    x[:, 1:] = x[:, :1] + torch.arange(1, E) * 2.0 ** -20
+    far = torch.arange(E) % 7 != 0  # the others stay near each other
+    s = np.stack([TO.scores(r, score) for r in x.numpy()])
+    bias = torch.from_numpy((s[3].max() - s[3]).astype(np.float32))
+    for top in (1, 2):
+        check_selection(M, T, E, 8, G, g, score, top, bias, x)
+        check_selection(M, T, E, 8, G, g, score, top, bias - 0.01 * far, x)
+
+
+@pytest.mark.parametrize("E,G,g", [(32, 8, 4), (256, 8, 4), (384, 8, 4), (60, 6, 3)])
+def test_route_groups_with_near_sums(M, E, G, g):
+    """No bias and groups by two scores: sigmoid(d) + sigmoid(-d) = 1 for every d, so groups
+    whose best logits are d and a hair more than -d differ by that hair alone."""
+    T, size = 64, E // G
+    gen = torch.Generator().manual_seed(E)
+    x = torch.full((T, G, size), -8.0) - torch.rand(T, G, size, generator=gen)
+    d = (torch.rand(T, G, generator=gen) * 64).round() / 64
+    hair = torch.randint(0, 64, (T, G), generator=gen) * 2.0 ** -24
+    x[:, :, 1] = d
+    x[:, :, size - 1] = -d + hair * (d > 0.3)
+    check_selection(M, T, E, 4, G, g, 0, 2, None, x.reshape(T, E).contiguous())
+
+
+@pytest.mark.parametrize("score", [0, 1])
+def test_gradient_where_one_share_is_nearly_all(M, score):
+    """Renormalised: a single place's gate is a constant, its gradient zero; of two places far
+    apart both gradients keep their relative precision (w1 w2 (g1 - g2): two shares of 64u,
+    a difference and products of a few u, under 256u)."""
+    T, E = 6, 48
+    x = logits_of(T, E, 3)
+    r = M.MoERouter(score, 1, 1)
+    out = torch.full((T, E), float("nan"), device="cuda")
+    M.moe_route_backward(config(M, T, E, 1), r, x.cuda(), x.argmax(1, keepdim=True).int().cuda(),
+                         torch.randn(T, 1).cuda(), out)
+    assert torch.count_nonzero(out) == 0
+    x[:, 7], x[:, 11] = 3.0, -torch.arange(T) * 3.0
+    idx = np.tile([7, 11], (T, 1))
+    dgate = torch.tensor([[1.0, -0.5]] * T)
+    M.moe_route_backward(config(M, T, E, 2), r, x.cuda(), torch.from_numpy(idx).int().cuda(),
+                         dgate.cuda(), out)
+    ref = TO.route_backward(x.numpy(), idx, dgate.numpy(), score, 1, RSF)
+    got = out.cpu().numpy()
+    assert np.all(np.abs(got - ref)[:, [7, 11]] <= 256 * U * np.abs(ref)[:, [7, 11]])
+    assert np.count_nonzero(got) == 2 * T
 
 
 @pytest.mark.parametrize("T,E,k", [(1, 2, 1), (5, 16, 4), (33, 60, 6), (40, 384, 8),
