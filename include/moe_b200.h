@@ -442,7 +442,7 @@ moe_status moe_route_scored(const moe_config* cfg, const moe_router* router, con
 
 /*
  * Gradient of moe_route_scored's gates with respect to the logits: dgate [T, top_k] fp32 ->
- * dlogits [T, E] fp32 (every element written).  The selection and the bias get no gradient
+ * dlogits [T, E] fp32 (every element written; not over the logits).  The selection and the bias get no gradient
  * (piecewise constant).  With g_j = routed_scaling_factor * dgate_j on the selected places:
  *   ds_j = (g_j - sum_i g_i s_i / S) / S with S = sum of the selected s (renormalize 1), or
  *   ds_j = g_j;
@@ -535,7 +535,7 @@ typedef enum { MOE_GRAD_FP32 = 0, MOE_GRAD_BF16 = 1 } moe_grad_dtype;
  */
 moe_status moe_muon_workspace_size(const moe_muon_config* cfg, size_t* bytes);
 
-/* out [groups, rows, cols] bf16 = the orthogonalised g (fp32 or bf16, g_dtype). */
+/* out [groups, rows, cols] bf16 = the orthogonalised g (fp32 or bf16, g_dtype; apart from out). */
 moe_status moe_orthogonalize(const moe_muon_config* cfg, const void* g, int32_t g_dtype, void* out,
                              void* workspace, size_t workspace_bytes, void* stream);
 

@@ -662,6 +662,7 @@ struct RouteBwdArgs {
   float* dlogits;            // [T, E] or null
   __nv_bfloat16* dense_b;    // the same as bf16 in rows of ld_b from column col_b, zeros to ld_b; or null
   int T, E, k, n_seq, col_b, ld_b;
+  int rows;                  // a warp's run
   float rsf;
   int score, renorm;
 };
@@ -777,111 +778,129 @@ __device__ __forceinline__ int sequence_of(const int32_t* off, int n_seq, int t)
   return lo;
 }
 
-// A warp per row.  Floor: 4E bytes read (where whole rows are needed) and 4E written a row.
+// A warp for a run of `rows` neighbouring rows: the sequence's coefficients stay in registers
+// from row to row.  Floor: 4E bytes read (where whole rows are needed) and 4E written a row;
+// instruction issue is what it spends its time on (32768 x 384, top 8, with the balance
+// loss's part: 32 us, 3.3 TB/s; a row a warp: 34).
 template <int PER, bool VEC>
-__global__ void __launch_bounds__(kRsWarps * 32) route_backward_kernel(const __grid_constant__ RouteBwdArgs a) {
+__global__ void __launch_bounds__(kRsWarps * 32, PER <= 12 ? 8 : 1) route_backward_kernel(const __grid_constant__ RouteBwdArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kRsWarps + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const int64_t base = static_cast<int64_t>(t) * a.E;
-  const float* row = a.logits + base;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRsWarps + (threadIdx.x >> 5)) * a.rows;
+  const int t_end = static_cast<int>(min(static_cast<int64_t>(a.T), t0 + a.rows));
   const bool soft = a.score == MOE_SCORE_SOFTMAX;
-  // the selected places: lane j holds place j
-  int e = lane < a.k ? __ldg(a.topk_idx + static_cast<int64_t>(t) * a.k + lane) : -1;
-  const float dg = lane < a.k ? __ldg(a.dgate + static_cast<int64_t>(t) * a.k + lane) : 0.f;
-  const int q = a.dscore ? sequence_of(a.seq_offsets, a.n_seq, t) : -1;
-  const bool whole = q >= 0 || (soft && !a.renorm);  // scores of the whole row are needed
-  float l[PER], s[PER], t1[PER], c[PER];
-  float lmax = -INFINITY, z = 0.f;
-  bool shifted = soft;
-  const float up = (q >= 0 && a.dloss) ? __ldg(a.dloss) : 1.f;
-  const float* crow = a.dscore + static_cast<int64_t>(q >= 0 ? q : 0) * a.E;
-  if (whole) {
-    load_row<PER, VEC>(row, a.E, lane, -INFINITY, l);
-    if (q >= 0) load_row<PER, VEC>(crow, a.E, lane, 0.f, c);
-  }
-  float lj = -INFINITY;
-  if (e >= 0 && e < a.E) lj = __ldg(row + e);
-  const bool have = lj > -INFINITY;
-  if (!have) e = -1 - lane;  // no expert: equal to no other place
-  if (whole) z = scores_of_row<PER>(soft, l, s, t1, lmax, shifted);
-  const float inv_z = z > 0.f ? 1.f / z : 0.f;
-  float csum = 0.f;  // sum c s'
-  if (q >= 0) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) csum = fmaf(c[i], s[i], csum);
-    csum = warp_sum(csum) * inv_z;
-  }
-  float g = have ? a.rsf * dg : 0.f;
-  float sj = 0.f, tj = 0.f;  // the place's sigmoid and 1 - sigmoid
-  if (!soft && have) sigmoid_both(lj, sj, tj);
-  const float mine = shifted ? (have ? exp_below<float>(lj, lmax) : 0.f) : sj;
-  float w = 0.f;  // renormalised: the place's share; otherwise its score
-  if (a.renorm) {
-    const float sum = soft ? 0.f : warp_sum(sj);
-    if (sum >= kTinySum) w = __fdividef(sj, sum);
-    else w = selected_share<float>(soft, have, lj);
-    // g_j - sum_i g_i w_i as sum_i w_i (g_j - g_i): a share near one does not cancel, and a
-    // single place's gradient is zero
-    float d = 0.f;
-    for (int i = 0; i < a.k; ++i) d = fmaf(__shfl_sync(kAll, w, i), g - __shfl_sync(kAll, g, i), d);
-    g = have ? d : 0.f;
-  } else if (have) {
-    w = soft ? mine * inv_z : sj;
-  }
-  const float dot = (soft && !a.renorm) ? warp_sum(g * w) : 0.f;  // sum ds p
-  // every expert of the row as if it were not selected
-  float* out = a.dlogits ? a.dlogits + base : nullptr;
-  __nv_bfloat16* brow = a.dense_b ? a.dense_b + static_cast<int64_t>(t) * a.ld_b + a.col_b : nullptr;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    float d = 0.f;
+  const float up = a.dscore && a.dloss ? __ldg(a.dloss) : 1.f;
+  float c[PER];
+  int q = -1, q_end = static_cast<int>(t0);  // q: the sequence of the rows before q_end
+  for (int t = static_cast<int>(t0); t < t_end; ++t) {
+    const int64_t base = static_cast<int64_t>(t) * a.E;
+    const float* row = a.logits + base;
+    // the selected places: lane j holds place j
+    int e = lane < a.k ? __ldg(a.topk_idx + static_cast<int64_t>(t) * a.k + lane) : -1;
+    const float dg = lane < a.k ? __ldg(a.dgate + static_cast<int64_t>(t) * a.k + lane) : 0.f;
+    if (a.dscore && t >= q_end) {
+      q = sequence_of(a.seq_offsets, a.n_seq, t);
+      q_end = q < 0 ? t + 1 : (a.seq_offsets ? __ldg(a.seq_offsets + q + 1) : a.T);
+      if (q >= 0) load_row<PER, VEC>(a.dscore + static_cast<int64_t>(q) * a.E, a.E, lane, 0.f, c);
+    }
+    const bool whole = q >= 0 || (soft && !a.renorm);  // scores of the whole row are needed
+    float l[PER], s[PER], t1[PER];
+    float lmax = -INFINITY, z = 0.f;
+    bool shifted = soft;
+    if (whole) load_row<PER, VEC>(row, a.E, lane, -INFINITY, l);
+    float lj = -INFINITY;
+    if (e >= 0 && e < a.E) lj = __ldg(row + e);
+    const bool have = lj > -INFINITY;
+    if (!have) e = -1 - lane;  // no expert: equal to no other place
+    if (whole) z = scores_of_row<PER>(soft, l, s, t1, lmax, shifted);
+    const float inv_z = z > 0.f ? 1.f / z : 0.f;
+    float csum = 0.f;  // sum c s'
     if (q >= 0) {
-      d = s[i] * inv_z * fmaf(up, c[i] - csum, -dot);
-      if (!soft) d *= t1[i];
-    } else if (whole) {  // a softmax
-      d = s[i] * (inv_z * -dot);
-    }
-    s[i] = d;
-  }
-  if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < PER; i += 4) {
-      const int ee = expert_of<PER, VEC>(lane, i);
-      if (out && ee < a.E) *reinterpret_cast<float4*>(out + ee) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+      for (int i = 0; i < PER; ++i) csum = fmaf(c[i], s[i], csum);
+      csum = warp_sum(csum) * inv_z;
     }
-  }
+    float g = have ? a.rsf * dg : 0.f;
+    float sj = 0.f, tj = 0.f;  // the place's sigmoid and 1 - sigmoid
+    if (!soft && have) sigmoid_both(lj, sj, tj);
+    const float mine = shifted ? (have ? exp_below<float>(lj, lmax) : 0.f) : sj;
+    float w = 0.f;       // renormalised: the place's share; otherwise its score
+    uint32_t same = 0u;  // places that name this one's expert
+    if (a.renorm) {
+      const float sum = soft ? 0.f : warp_sum(sj);
+      if (sum >= kTinySum) w = __fdividef(sj, sum);
+      else w = selected_share<float>(soft, have, lj);
+      // g_j - sum_i g_i w_i as sum_i w_i (g_j - g_i): a share near one does not cancel, and a
+      // single place's gradient is zero
+      float d = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < a.k; ++i) {
+        d = fmaf(__shfl_sync(kAll, w, i), g - __shfl_sync(kAll, g, i), d);
+        same |= __shfl_sync(kAll, e, i) == e ? 1u << i : 0u;
+      }
+      g = have ? d : 0.f;
+    } else {
+      if (have) w = soft ? mine * inv_z : sj;
+#pragma unroll 4
+      for (int i = 0; i < a.k; ++i) same |= __shfl_sync(kAll, e, i) == e ? 1u << i : 0u;
+    }
+    const float dot = (soft && !a.renorm) ? warp_sum(g * w) : 0.f;  // sum ds p
+    // every expert of the row as if it were not selected
+    if (q >= 0) {
+      const float f = inv_z * up, h = inv_z * fmaf(up, csum, dot);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int ee = expert_of<PER, VEC>(lane, i);
-    if (!VEC && out && ee < a.E) out[ee] = s[i];
-    if (brow && ee < a.ld_b - a.col_b) brow[ee] = __float2bfloat16_rn(ee < a.E ? s[i] : 0.f);
-  }
-  if (brow)
-    for (int ee = lane + 32 * PER; ee < a.ld_b - a.col_b; ee += 32) brow[ee] = __float2bfloat16_rn(0.f);
-  // the selected ones over it (the warp's stores above come first); places that name the
-  // same expert add up
-  float gs = 0.f;
-  bool first = true;
-  for (int j = 0; j < a.k; ++j) {
-    const int ej = __shfl_sync(kAll, e, j);
-    const float gj = __shfl_sync(kAll, g, j);
-    if (ej == e) {
-      gs += gj;
-      if (j < lane) first = false;
+      for (int i = 0; i < PER; ++i) {
+        s[i] *= fmaf(f, c[i], -h);
+        if (!soft) s[i] *= t1[i];
+      }
+    } else {  // a softmax, or nothing
+      const float h = whole ? inv_z * -dot : 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) s[i] = whole ? s[i] * h : 0.f;
     }
-  }
-  __syncwarp();
-  if (have && first) {
-    float d = 0.f;
-    if (whole) d = mine * inv_z * ((q >= 0 ? up * (__ldg(crow + e) - csum) : 0.f) - dot);
-    d = fmaf(gs, w, d);
-    if (!soft) d *= tj;
-    if (out) out[e] = d;
-    if (brow) brow[e] = __float2bfloat16_rn(d);
+    float* out = a.dlogits ? a.dlogits + base : nullptr;
+    __nv_bfloat16* brow = a.dense_b ? a.dense_b + static_cast<int64_t>(t) * a.ld_b + a.col_b : nullptr;
+    if (out) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int ee = expert_of<PER, VEC>(lane, i);
+        if constexpr (VEC) {
+          if (i % 4 == 0 && ee < a.E)
+            *reinterpret_cast<float4*>(out + ee) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+        } else {
+          if (ee < a.E) out[ee] = s[i];
+        }
+      }
+    }
+    if (brow) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int ee = expert_of<PER, VEC>(lane, i);
+        if (ee < a.ld_b - a.col_b) brow[ee] = __float2bfloat16_rn(ee < a.E ? s[i] : 0.f);
+      }
+      for (int ee = lane + 32 * PER; ee < a.ld_b - a.col_b; ee += 32) brow[ee] = __float2bfloat16_rn(0.f);
+    }
+    // the selected ones over it (the warp's stores above come first); places that name the
+    // same expert add up
+    float gs = g;
+    if (__any_sync(kAll, have && (same & (same - 1u)) != 0u)) {
+      gs = 0.f;
+      for (int i = 0; i < a.k; ++i) {
+        const float gi = __shfl_sync(kAll, g, i);
+        if ((same >> i) & 1u) gs += gi;
+      }
+    }
+    __syncwarp();
+    if (have && __ffs(same) - 1 == lane) {
+      float d = 0.f;
+      if (whole) d = mine * inv_z * ((q >= 0 ? up * (__ldg(a.dscore + static_cast<int64_t>(q) * a.E + e) - csum) : 0.f) - dot);
+      d = fmaf(gs, w, d);
+      if (!soft) d *= tj;
+      if (out) out[e] = d;
+      if (brow) brow[e] = __float2bfloat16_rn(d);
+    }
   }
 }
 
@@ -928,16 +947,17 @@ __device__ __forceinline__ int seq_tiles(const BalanceArgs& a, int q) {
   return (hi - lo + a.tile_rows - 1) / a.tile_rows;
 }
 
-// Sum of seq_tiles over q < n, by the whole block (every thread gets it).
+// Sum of seq_tiles over q < n, by the whole block (every thread gets it); at most a.tiles, as
+// it is for ascending offsets, whatever the offsets are.
 __device__ __forceinline__ int tiles_before(const BalanceArgs& a, int n, int* sh) {
-  int v = 0;
-  for (int q = threadIdx.x; q < n; q += blockDim.x) v += seq_tiles(a, q);
-  v = warp_sum(v);
+  int64_t all = 0;
+  for (int q = threadIdx.x; q < n; q += blockDim.x) all += seq_tiles(a, q);
+  const int v = static_cast<int>(min(warp_sum(all), static_cast<int64_t>(a.tiles)));
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
   __syncthreads();
   int s = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += sh[w];
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s = min(s + sh[w], a.tiles);
   __syncthreads();
   return s;
 }
@@ -989,7 +1009,8 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_rows_kernel(const __gr
   }
   int lo, hi;
   seq_bounds(a, q, lo, hi);
-  lo += (blockIdx.x - first) * a.tile_rows;
+  // (inside the sequence whatever the offsets are)
+  lo = max(lo, lo + (static_cast<int>(blockIdx.x) - first) * a.tile_rows);
   hi = min(hi, lo + a.tile_rows);
   for (int i = threadIdx.x; i < PER * 32; i += blockDim.x) hist[i] = 0;
   if (threadIdx.x == 0) rows_ok = 0;

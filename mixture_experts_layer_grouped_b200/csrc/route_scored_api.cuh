@@ -109,7 +109,11 @@ moe_status do_route_backward(const moe_config& c, const moe_router& r, const flo
     if constexpr (PER % 4 == 0) {
       if (vec) kern = route_backward_kernel<PER, true>;
     }
-    MOE_TRY(launch_pdl(kern, dim3((c.T + kRsWarps - 1) / kRsWarps), dim3(kRsWarps * 32), 0, s, a));
+    // one wave of 32 warps an SM, equal runs
+    const int blocks = (c.T + kRsWarps - 1) / kRsWarps, wave = 8 * sm_count();
+    a.rows = (blocks + wave - 1) / wave;
+    const int warps = (c.T + a.rows - 1) / a.rows;
+    MOE_TRY(launch_pdl(kern, dim3((warps + kRsWarps - 1) / kRsWarps), dim3(kRsWarps * 32), 0, s, a));
     return launch_check();
   });
 }
