@@ -672,6 +672,7 @@ class MoETrainLayer(MoELayer):
             raise ValueError("balance_coef needs a router (MoERouter)")
         self.balance_coef = balance_coef
         self.balance = None
+        self._balances = {}
         self.seq_offsets = None
         self.bwd_weights = prepare_backward_weights(cfg, weights, w_router)
         nbytes, r_cap = moe_workspace_size(cfg)
@@ -691,9 +692,11 @@ class MoETrainLayer(MoELayer):
                            if cfg.I_shared > 0 else None)
 
     def _balance_buffers(self, n_seq):
-        if self.balance is None or self.balance["load"].shape[0] != n_seq:
+        # one set for each number of sequences, kept: a captured graph may hold any of them
+        self.balance = self._balances.get(n_seq)
+        if self.balance is None:
             c, dev = self.cfg, self.saved["logits"].device
-            self.balance = {
+            self.balance = self._balances[n_seq] = {
                 "loss": torch.empty(1, dtype=torch.float32, device=dev),
                 "load": torch.empty(n_seq, c.E, dtype=torch.int32, device=dev),
                 "dscore": torch.empty(n_seq, c.E, dtype=torch.float32, device=dev),

@@ -77,8 +77,10 @@ __global__ void __launch_bounds__(256) muon_norm_kernel(const __grid_constant__ 
   pdl_trigger();
   __shared__ double red[8];
   const int mat = blockIdx.y;
-  if (blockIdx.x == 0 && mat == 0)
-    for (int i = threadIdx.x; i < a.n_counters; i += 256) a.counters[i] = 0;
+  const int64_t threads = static_cast<int64_t>(gridDim.x) * gridDim.y * 256;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+       i < a.n_counters; i += threads)
+    a.counters[i] = 0;
   const int64_t base = static_cast<int64_t>(mat) * a.n;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
   const int64_t i1 = min(i0 + a.chunk, a.n);

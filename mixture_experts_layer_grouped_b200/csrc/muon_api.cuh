@@ -8,6 +8,7 @@ namespace {
 struct MuonLayout {
   size_t status, counters, part, x[2][2], a[2], b[2], diag[2], partial, total;  // [buffer][hi, lo], [hi, lo]
   int r, ld, ldr, chunk, chunks;
+  int64_t units;  // of all steps
   int tile, sym_n, sym_tiles, app_n, app_tiles, k_gram, k_r, splits, sums, n_counters;
 };
 
@@ -125,6 +126,8 @@ MuonLayout muon_layout(const moe_muon_config& c) {
   L.n_counters = static_cast<int>(1 + G * 3 * c.steps + (L.splits > 1 ? G * L.sym_tiles : 0));
   const size_t xb = G * static_cast<size_t>(c.rows) * L.ld * 2;
   const size_t ab = G * static_cast<size_t>(L.r) * L.ldr * 2;
+  L.units = static_cast<int64_t>(c.groups) * c.steps *
+            (static_cast<int64_t>(L.sym_tiles) * (L.splits + L.sums + 1) + L.app_tiles);
   size_t o = 0;
   L.status = o; o = align_up(o + 4);
   L.counters = o; o = align_up(o + static_cast<size_t>(L.n_counters) * 4);
@@ -151,6 +154,7 @@ moe_status check_muon(const moe_muon_config* c) {
   if (static_cast<int64_t>(c->rows) * ((static_cast<int64_t>(c->cols) + 7) / 8 * 8) > (int64_t(1) << 30))
     return MOE_ERR_UNSUPPORTED;
   if (!muon_bounds(*c).ok) return MOE_ERR_UNSUPPORTED;
+  if (!muon_small(*c) && muon_layout(*c).units > (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -266,10 +270,7 @@ moe_status ns_steps(const moe_muon_config& c, const MuonArgs& u, const MuonLayou
   p.k_r = L.k_r;
   p.splits = L.splits;
   p.sums = L.sums;
-  const int64_t total = static_cast<int64_t>(c.groups) * c.steps *
-                        (static_cast<int64_t>(L.sym_tiles) * (L.splits + L.sums + 1) + L.app_tiles);
-  if (total > (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
-  p.total = static_cast<int32_t>(total);
+  p.total = static_cast<int32_t>(L.units);
   int32_t* counters = reinterpret_cast<int32_t*>(b + L.counters);
   p.unit_counter = counters;
   p.done = counters + 1;

@@ -145,10 +145,56 @@ def test_masked_tokens_pass_the_layer(M):
     assert rel_frob(f64(y1), ref) <= 1e-2 and torch.isfinite(y0).all()
 
 
-def test_training_steps_with_muon(M):
+@pytest.mark.parametrize("dtype", ["mxfp8", "nvfp4"])
+def test_block_scaled_layers_take_the_router(M, dtype):
+    """The scored router in the block-scaled layers: the plain layer's results where the two
+    routers are the same (up to fp32 roundings of the gates)."""
+    cfg = synth.get_config("tiny_bf16_T64").scaled(dtype=dtype, H=256, I=256, I_shared=256,
+                                                    pad_multiple=128)
+    d = synth.gen_all(cfg, "cuda")
+    c = M.config_from_shape(cfg)
+    ys = [M.MoELayer(c, weights_dict(d), d["w_router"], d["bias"], router=r).forward(d["x"])
+          for r in (None, M.MoERouter(0, 1, 2))]
+    assert rel_frob(f64(ys[1]), f64(ys[0])) <= 1e-3
+
+
+def test_captured_steps_of_different_sequences(M):
+    """Two captured training steps of one layer, with one and with three sequences, replayed in
+    turn: each gives what the eager step gives, the loss and the gradients among them."""
+    cfg = shape()
+    d = synth.gen_all(cfg, "cuda")
+    c, r = M.config_from_shape(cfg), M.MoERouter(0, 1, 1)
+    layer = M.MoETrainLayer(c, weights_dict(d), d["w_router"], None, router=r, balance_coef=0.3)
+    dy = synth.gen_dy(cfg, "cuda")
+    offs = [None, torch.tensor([0, 20, 20, 60], dtype=torch.int32, device="cuda")]
+    out = torch.empty_like(d["x"])
+
+    def step(off):
+        layer.forward(d["x"], out=out, seq_offsets=off)
+        g = layer.backward(dy)
+        return {**g, "loss": layer.balance["loss"], "load": layer.balance["load"], "y": out}
+
+    eager = [{k: v.clone() for k, v in step(off).items()} for off in offs]
+    graphs, held = [], []
+    for off in offs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(step(off))
+    for i in (0, 1, 0):
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        for k, v in eager[i].items():
+            assert rel_frob(f64(held[i][k]), f64(v)) <= 1e-6, k
+        assert torch.equal(held[i]["load"], eager[i]["load"])
+    assert layer.device_status() == 0
+    del graphs
+
+
+@pytest.mark.parametrize("shared", [0, 128])
+def test_training_steps_with_muon(M, shared):
     """Forward, balance loss, backward, Muon on every weight, and the next forward with the
     new weights; the updated weights against the oracle given the same gradients."""
-    cfg = shape(I_shared=128)
+    cfg = shape(I_shared=shared)
     d = synth.gen_all(cfg, "cuda")
     c, r = M.config_from_shape(cfg), M.MoERouter(1, 1, 1)
     weights = weights_dict(d)
