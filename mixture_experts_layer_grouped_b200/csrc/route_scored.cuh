@@ -326,19 +326,23 @@ __device__ __noinline__ void route_row_64(const ScoredArgs& a, int t, const floa
   }
 }
 
-// e^x and 1 / (1 + e^-x) from the hardware's approximations, for keys alone.  ex2.approx is
-// within 2^-22 of itself (and its argument's rounding adds |x| 2^-24), rcp.approx within 2^-23,
-// so a sigmoid is off by at most s (1 - s) (2^-22 + |x| 2^-24) + s (2^-23 + 2^-24) < 2.6e-7.
-__device__ __forceinline__ float exp_fast(float x) {
+// 2^x and 1 / x from the hardware (2^-22 and 2^-23 of the result); no result is subnormal.
+__device__ __forceinline__ float ex2_fast(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float sigmoid_fast(float x) {
+__device__ __forceinline__ float rcp_fast(float x) {
   float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + exp_fast(-x)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// e^x and 1 / (1 + e^-x) from them, for keys alone.  The exponential's argument's rounding
+// adds |x| 2^-24, so a sigmoid is off by at most
+// s (1 - s) (2^-22 + |x| 2^-24) + s (2^-23 + 2^-24) < 2.6e-7.
+__device__ __forceinline__ float exp_fast(float x) { return ex2_fast(x * 1.4426950408889634f); }
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.f + exp_fast(-x)); }
 
 constexpr int kRsCand = 64;  // candidates of a row
 
@@ -693,18 +697,6 @@ __device__ __forceinline__ void load_row(const float* row, int E, int lane, floa
       v[i] = e < E ? __ldg(row + e) : fill;
     }
   }
-}
-
-// 2^x and 1 / x from the hardware (2^-22 and 2^-23 of the result); no result is subnormal.
-__device__ __forceinline__ float ex2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // sigmoid(l) and 1 - sigmoid(l), each to its own precision: with q = exp(-|l|), 1 / (1 + q)
