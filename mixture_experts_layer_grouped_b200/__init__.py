@@ -1,5 +1,6 @@
 """Routed Mixture-of-Experts layer on one B200 (sm_100a): the forward, and the
-backward of the bf16 layer.
+backward of the bf16 layer; routing by softmax or sigmoid scores with its gradient
+and a balance loss; and Muon updates of the weights.
 
 A thin ctypes binding over ``libmoe_b200.so``: the functions below marshal
 torch tensors into device pointers and call the C ABI of include/moe_b200.h

@@ -425,6 +425,11 @@ __device__ __forceinline__ void counter_add(int32_t* p) {
 // the others where the warp's blocks of a tile fit its buffers, otherwise while the next
 // blocks are worked on.  Loads and stores clip at the matrix's edges.  (Plain
 // loads and stores, one row a lane: 18 us a 256 x 256 tile, of which the products need 4.3.)
+//
+// Bound: 64 x [2048, 1024] 2.9 ms (0.82 PFLOP/s of the formulas' products), 32 x [2048, 4096] 9.0 ms
+// (1.07 PFLOP/s): a k-step of a pair takes 670-780 clocks for its 64 KB from L2, 512 of the tensor
+// pipe, at the clock that the power cap leaves.  One small stack or matrix: 15 dependent products
+// of 7 to 14 us, most of it a unit's way in and out.
 template <bool TALL, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(kNsThreads, 1) ns_steps_kernel(const __grid_constant__ NsParams p) {
   constexpr int TILE = PAIR ? 256 : 128;

@@ -13,6 +13,8 @@
 // Every product takes fp16 hi and lo parts (hi hi + hi lo + lo hi, 22 bits): the square roots
 // of S's roundings are what small singular values see, and with 11 bits those would be gone.
 // Measured against 64 bits: 1e-6 (full rank) to 1e-3 (rank 1), far below the bf16 result.
+// Measured: 16 x [128, 256] fp32 58 us (the chain takes most of it);
+// 64 x [100, 7000] with momentum and weights 0.40 ms (1.1 GB: 2.7 TB/s).
 // The pieces are scaled by a power of two from their largest value; partial sums carry the
 // exponent, so the range of fp32 gradients is covered.
 #pragma once
@@ -345,6 +347,8 @@ __global__ void __launch_bounds__(kMsThreads, 1) muon_gram_kernel(const __grid_c
 // One CTA a matrix.  A thread holds a quarter of a row of S in fp32; P, Q and S (or P S) live
 // in shared memory as image pairs.  Three dependent products a step: at r = 128 each reads
 // 192 KB of shared memory (1536 clk of its bandwidth) and 256 KB of new images are written.
+// Latency: 48 us for the 14 of five steps, however few the matrices.  (r <= 32 in fp32 on the
+// ordinary cores: 16 rows 29 -> 24 us a call, but 64 x [32, 2000] 74 -> 81.)
 __global__ void __launch_bounds__(kMsThreads, 1) muon_chain_kernel(const __grid_constant__ MuonSmallArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = ms_smem(smem_raw);
