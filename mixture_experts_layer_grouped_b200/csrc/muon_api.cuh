@@ -105,11 +105,17 @@ MuonLayout muon_layout(const moe_muon_config& c) {
   L.chunk = static_cast<int>(chunk);
   L.chunks = static_cast<int>((n + chunk - 1) / chunk);
   const bool split = muon_split(c);
-  // 256 x 256 tiles by CTA pairs where they fill the GPU, one-CTA 128 x 128 tiles otherwise
-  // (each is done sooner, and there are more of them)
+  // 256 x 256 tiles by CTA pairs, which read half as much per product, where they fill the GPU
+  // and are not mostly edge: 128 x 128 tiles of one CTA where there are at most three of them
+  // for one of the large.  (Small against large: three each at 64 x [384, 2048] 1.24 and 1.33 ms,
+  // 2.8 at 8 x [640, 640] 0.17 and 0.20; 3.4 at 16 x [1300, 1300] 1.73 and 1.43, four at
+  // 16 x [1024, 1024] 0.71 and 0.57.)
   auto tiles = [&](int v) { return (v + L.tile - 1) / L.tile; };
+  L.tile = 128;
+  const int64_t small = static_cast<int64_t>(tiles(c.rows)) * tiles(c.cols);
   L.tile = 256;
-  if (split || G * tiles(c.rows) * tiles(c.cols) < 74) L.tile = 128;
+  const int64_t large = static_cast<int64_t>(tiles(c.rows)) * tiles(c.cols);
+  if (split || static_cast<int64_t>(G) * large < 74 || small <= 3 * large) L.tile = 128;
   L.sym_n = tiles(L.r);
   L.sym_tiles = L.sym_n * (L.sym_n + 1) / 2;
   L.app_n = tiles(c.cols);

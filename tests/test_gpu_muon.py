@@ -62,6 +62,8 @@ SHAPES = [  # groups, rows, cols
     (1, 1, 1), (3, 1, 7), (2, 5, 1), (2, 8, 8), (3, 17, 130), (2, 130, 17), (2, 128, 256),
     (2, 256, 128), (1, 129, 64), (2, 64, 129), (1, 200, 333), (2, 300, 130), (3, 256, 512),
     (1, 512, 257), (1, 130, 1100), (1, 1100, 131), (40, 136, 136), (1, 384, 2056), (2, 515, 515),
+    # tiles of CTA pairs: one a matrix, several with a mirrored one, split along the contraction
+    (80, 136, 136), (80, 150, 132), (20, 500, 512), (20, 512, 505), (10, 505, 1100), (10, 1100, 505),
 ]
 
 
